@@ -22,6 +22,13 @@ EP_MXFP8_E4M3 = 3
 EP_F16 = 4
 EP_SCALES_MN_MAJOR = 0x100   # OR-ed into an FP8 dtype: scales stored transposed
 EP_READ_X_AHEAD = 0x200      # OR-ed into ep_layout_dispatch's dtype: x read into the MALL during the layout
+EP_GRAD_F32 = 0x400          # OR-ed into a weights' gradient's dtype: fp32 gradients
+EP_GRAD_ACCUMULATE = 0x800   # OR-ed into it: added to what the gradients hold
+EP_ACT_NONE = 0
+EP_ACT_RELU = 1
+EP_ACT_GELU = 2
+EP_ACT_SILU = 3
+EP_ACT_SWIGLU = 4
 _FP8_DTYPES = (EP_FP8_E4M3, EP_FP8_E4M3_POW2, EP_MXFP8_E4M3)
 EP_FLAG_BAD_EXPERT = 1
 EP_FLAG_OVERFLOW = 2
@@ -78,6 +85,14 @@ SIGNATURES = {
     "ep_dequant_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
     "ep_cast_e4m3_bits": (ctypes.c_int, [_u32, _i64, _i32, _vp, _vp]),
     "ep_copy": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
+    "ep_expert_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _LP, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_expert_gemm_grad_x": (ctypes.c_int, [_vp, _vp, _LP, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_expert_gemm_grad_w": (ctypes.c_int, [_vp, _vp, _LP, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_linear": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_linear_grad_x": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_linear_grad_w": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_act_grad": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "ep_combine_grad": (ctypes.c_int, [_vp, _vp, _vp, _LP, _i32, _i32, _vp, _vp, _vp]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ep_version": (ctypes.c_char_p, []),
 }
@@ -383,6 +398,208 @@ def ep_combine_groups(z: torch.Tensor, layout: EpGroupLayout, out: torch.Tensor,
     _check("ep_combine_groups", lib().ep_combine_groups(
         _ptr(z, "z", torch.bfloat16), ctypes.byref(layout.struct), H,
         _ptr(out, "out", torch.bfloat16), _stream(stream)))
+
+
+# The matrix products and the gradients.  Their tensors may live on any one GPU: the call
+# runs there, on the given stream or that GPU's current one.
+def _elem(dtype: int) -> torch.dtype:
+    return torch.float16 if dtype == EP_F16 else torch.bfloat16
+
+
+def _width(n: int, act: int) -> int:
+    return 2 * n if act == EP_ACT_SWIGLU else n
+
+
+def _operand(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, device) -> int | None:
+    """Device pointer of a contiguous tensor of this type, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr() if t.numel() else None
+
+
+def _call(fn: str, device: torch.device, stream, *args) -> None:
+    """The entry point on `device`, with the stream as its last argument."""
+    f = getattr(lib(), fn)
+    if device.index == torch.cuda.current_device():
+        status = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream(stream))
+    _check(fn, status)
+
+
+def _on_gpu(t: torch.Tensor, name: str, dims: int) -> torch.device:
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions" % (name, dims))
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    return t.device
+
+
+def _layout_on(layout: EpLayout, device: torch.device) -> None:
+    if layout.expert_offsets.device != device:
+        raise ValueError("the layout is on %s, the tensors on %s" % (layout.expert_offsets.device, device))
+
+
+def _distinct(out: torch.Tensor | None, name: str, *inputs: torch.Tensor | None) -> None:
+    """An output that shares memory with an input is refused."""
+    if out is None:
+        return
+    a, n = out.data_ptr(), out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < a + n:
+            raise ValueError("%s overlaps an input" % name)
+
+
+def ep_expert_gemm(x: torch.Tensor, weights: torch.Tensor, layout: EpLayout, out: torch.Tensor,
+                   dtype: int, act: int = EP_ACT_NONE, x_scales: torch.Tensor | None = None,
+                   weight_scales: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   preact: torch.Tensor | None = None, stream=None) -> None:
+    """x [R, K] (what ep_dispatch wrote with this dtype), weights [E, W, K] -> out [R, N]:
+    act(x W_e^T + bias_e) for the rows of each expert e; W = N, or 2N for EP_ACT_SWIGLU.
+    bf16 / fp16: all of that type.  FP8: uint8 codes, x_scales fp32 [R, K/128] ([K/128, R] with
+    EP_SCALES_MN_MAJOR), weight_scales fp32 [E, W/128, K/128].  MXFP8: x_scales uint8 [R, K/32],
+    weight_scales uint8 [E, W, K/32].  FP8 results are bf16.  preact [R, W]: the product itself."""
+    dev = _on_gpu(x, "x", 2)
+    _layout_on(layout, dev)
+    R, E, K, N = layout.num_recv_rows, layout.num_experts, x.shape[1], out.shape[-1]
+    W, base = _width(N, act), dtype & ~EP_SCALES_MN_MAJOR
+    fp8, et = base in _FP8_DTYPES, _elem(base)
+    qt = torch.uint8 if fp8 else et
+    if fp8:
+        mx = base == EP_MXFP8_E4M3
+        st = torch.uint8 if mx else torch.float32
+        xs = (R, K // 32) if mx else (K // 128, R) if dtype & EP_SCALES_MN_MAJOR else (R, K // 128)
+        ws = (E, W, K // 32) if mx else (E, W // 128, K // 128)
+    else:
+        st, xs, ws = torch.float32, (), ()
+        if x_scales is not None or weight_scales is not None:
+            raise ValueError("dtype %d has no scales" % dtype)
+    _distinct(out, "out", x, weights, bias, x_scales, weight_scales, preact)
+    _distinct(preact, "preact", x, weights, bias, x_scales, weight_scales)
+    _call("ep_expert_gemm", dev, stream, _operand(x, "x", qt, (R, K), dev),
+          _operand(x_scales, "x_scales", st, xs, dev),
+          _operand(weights, "weights", qt, (E, W, K), dev),
+          _operand(weight_scales, "weight_scales", st, ws, dev),
+          _operand(bias, "bias", et, (E, W), dev), ctypes.byref(layout.struct), K, N, dtype, act,
+          _operand(preact, "preact", et, (R, W), dev), _operand(out, "out", et, (R, N), dev))
+
+
+def ep_expert_gemm_grad_x(dy: torch.Tensor, weights: torch.Tensor, layout: EpLayout,
+                          dx: torch.Tensor, dtype: int, act: int = EP_ACT_NONE,
+                          preact: torch.Tensor | None = None, stream=None) -> None:
+    """dy [R, N], weights [E, N, K] -> dx = (dy W_e) act'(preact): [R, K], or with EP_ACT_SWIGLU
+    [R, 2K]; preact has dx's shape (none for EP_ACT_NONE)."""
+    dev = _on_gpu(dy, "dy", 2)
+    _layout_on(layout, dev)
+    if weights.dim() != 3:
+        raise ValueError("weights must have 3 dimensions")
+    R, E, N, K, et = layout.num_recv_rows, layout.num_experts, dy.shape[1], weights.shape[2], _elem(dtype)
+    shape = (R, _width(K, act))
+    _distinct(dx, "dx", dy, weights, preact)
+    _call("ep_expert_gemm_grad_x", dev, stream, _operand(dy, "dy", et, (R, N), dev),
+          _operand(weights, "weights", et, (E, N, K), dev), ctypes.byref(layout.struct), K, N, dtype,
+          act, _operand(preact, "preact", et, shape, dev), _operand(dx, "dx", et, shape, dev))
+
+
+def ep_expert_gemm_grad_w(dy: torch.Tensor, x: torch.Tensor, layout: EpLayout,
+                          dweights: torch.Tensor, dtype: int, dbias: torch.Tensor | None = None,
+                          stream=None) -> None:
+    """dy [R, N], x [R, K] -> dweights [E, N, K] (and dbias [E, N]): dy_e^T x_e over the rows of
+    each expert, in dtype's type or, with EP_GRAD_F32, fp32; EP_GRAD_ACCUMULATE adds."""
+    dev = _on_gpu(dy, "dy", 2)
+    _layout_on(layout, dev)
+    R, E, N, K = layout.num_recv_rows, layout.num_experts, dy.shape[1], x.shape[-1]
+    et = _elem(dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE))
+    gt = torch.float32 if dtype & EP_GRAD_F32 else et
+    _distinct(dweights, "dweights", dy, x, dbias)
+    _distinct(dbias, "dbias", dy, x)
+    _call("ep_expert_gemm_grad_w", dev, stream, _operand(dy, "dy", et, (R, N), dev),
+          _operand(x, "x", et, (R, K), dev), ctypes.byref(layout.struct), K, N, dtype,
+          _operand(dweights, "dweights", gt, (E, N, K), dev), _operand(dbias, "dbias", gt, (E, N), dev))
+
+
+def ep_linear(x: torch.Tensor, weights: torch.Tensor, out: torch.Tensor, dtype: int,
+              act: int = EP_ACT_NONE, bias: torch.Tensor | None = None,
+              residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+              stream=None) -> None:
+    """x [rows, K], weights [W, K] -> out [rows, N] = act(x W^T + bias) + residual; W = N, or 2N
+    for EP_ACT_SWIGLU.  preact [rows, W]: the product itself.  out may be the residual."""
+    dev = _on_gpu(x, "x", 2)
+    T, K, N, et = x.shape[0], x.shape[1], out.shape[-1], _elem(dtype)
+    W = _width(N, act)
+    _distinct(out, "out", x, weights, bias, preact,
+              None if residual is not None and residual.data_ptr() == out.data_ptr() else residual)
+    _distinct(preact, "preact", x, weights, bias, residual)
+    _call("ep_linear", dev, stream, _operand(x, "x", et, (T, K), dev),
+          _operand(weights, "weights", et, (W, K), dev), _operand(bias, "bias", et, (W,), dev),
+          _operand(residual, "residual", et, (T, N), dev), T, K, N, dtype, act,
+          _operand(preact, "preact", et, (T, W), dev), _operand(out, "out", et, (T, N), dev))
+
+
+def ep_linear_grad_x(dy: torch.Tensor, weights: torch.Tensor, dx: torch.Tensor, dtype: int,
+                     act: int = EP_ACT_NONE, preact: torch.Tensor | None = None, stream=None) -> None:
+    """dy [rows, N], weights [N, K] -> dx = (dy W) act'(preact), as ep_expert_gemm_grad_x."""
+    dev = _on_gpu(dy, "dy", 2)
+    if weights.dim() != 2:
+        raise ValueError("weights must have 2 dimensions")
+    T, N, K, et = dy.shape[0], dy.shape[1], weights.shape[1], _elem(dtype)
+    shape = (T, _width(K, act))
+    _distinct(dx, "dx", dy, weights, preact)
+    _call("ep_linear_grad_x", dev, stream, _operand(dy, "dy", et, (T, N), dev),
+          _operand(weights, "weights", et, (N, K), dev), T, K, N, dtype, act,
+          _operand(preact, "preact", et, shape, dev), _operand(dx, "dx", et, shape, dev))
+
+
+def ep_linear_grad_w(dy: torch.Tensor, x: torch.Tensor, dweights: torch.Tensor, dtype: int,
+                     dbias: torch.Tensor | None = None, stream=None) -> None:
+    """dy [rows, N], x [rows, K] -> dweights [N, K] = dy^T x, dbias [N], as ep_expert_gemm_grad_w."""
+    dev = _on_gpu(dy, "dy", 2)
+    T, N, K = dy.shape[0], dy.shape[1], x.shape[-1]
+    et = _elem(dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE))
+    gt = torch.float32 if dtype & EP_GRAD_F32 else et
+    _distinct(dweights, "dweights", dy, x, dbias)
+    _distinct(dbias, "dbias", dy, x)
+    _call("ep_linear_grad_w", dev, stream, _operand(dy, "dy", et, (T, N), dev),
+          _operand(x, "x", et, (T, K), dev), T, K, N, dtype,
+          _operand(dweights, "dweights", gt, (N, K), dev), _operand(dbias, "dbias", gt, (N,), dev))
+
+
+def ep_act_grad(dy: torch.Tensor, preact: torch.Tensor, dz: torch.Tensor, dtype: int, act: int,
+                stream=None) -> None:
+    """dz = dy act'(preact): dy [rows, n], preact and dz [rows, n] ([rows, 2n] for EP_ACT_SWIGLU)."""
+    dev = _on_gpu(dy, "dy", 2)
+    T, n, et = dy.shape[0], dy.shape[1], _elem(dtype)
+    shape = (T, _width(n, act))
+    _call("ep_act_grad", dev, stream, _operand(dy, "dy", et, (T, n), dev),
+          _operand(preact, "preact", et, shape, dev), T, n, dtype, act,
+          _operand(dz, "dz", et, shape, dev))
+
+
+def ep_combine_grad(dout: torch.Tensor, expert_out: torch.Tensor | None, topk_weights: torch.Tensor,
+                    layout: EpLayout, d_expert_out: torch.Tensor,
+                    d_topk_weights: torch.Tensor | None, dtype: int, stream=None) -> None:
+    """Gradients of ep_combine (EP_BF16) or ep_combine_f16 (EP_F16): dout [T, H] -> d_expert_out
+    [R, H] (used rows) and d_topk_weights fp32 [T, k] (None to skip; expert_out is then unused)."""
+    dev = _on_gpu(dout, "dout", 2)
+    _layout_on(layout, dev)
+    T, k, R, H, et = layout.num_tokens, layout.num_topk, layout.num_recv_rows, dout.shape[1], _elem(dtype)
+    _distinct(d_expert_out, "d_expert_out", dout, expert_out, topk_weights, d_topk_weights)
+    _call("ep_combine_grad", dev, stream, _operand(dout, "dout", et, (T, H), dev),
+          _operand(expert_out, "expert_out", et, (R, H), dev),
+          _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev),
+          ctypes.byref(layout.struct), H, dtype, _operand(d_expert_out, "d_expert_out", et, (R, H), dev),
+          _operand(d_topk_weights, "d_topk_weights", torch.float32, (T, k), dev))
 
 
 def ep_dequant_fp8(q: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:

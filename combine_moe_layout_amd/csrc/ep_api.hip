@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "ep_gemm.h"
 #include "ep_internal.h"
 
 namespace {
@@ -108,6 +109,101 @@ int check_dispatch(const void* x, const ep_layout_t* layout, int32_t hidden, int
       (fp8 && (reinterpret_cast<uintptr_t>(recv_scales) & 3u) != 0))
     return EP_ERR_ALIGN;
   return EP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Matrix products.
+bool feature_size(int32_t n, int32_t multiple) {
+  return n >= 8 && n <= EP_MAX_HIDDEN && n % multiple == 0;
+}
+bool known_act(int32_t act) { return act >= EP_ACT_NONE && act <= EP_ACT_SWIGLU; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The groups of a layout's receive rows.
+int layout_groups(const ep_layout_t* layout, ep::RowGroups* g) {
+  const int rc = check_layout(layout);
+  if (rc != EP_OK) return rc;
+  if (layout->expert_offsets == nullptr || layout->num_tokens_per_expert == nullptr)
+    return EP_ERR_NULL;
+  *g = ep::RowGroups{layout->expert_offsets, layout->num_tokens_per_expert, layout->num_experts,
+                     layout->capacity, layout->num_recv_rows,
+                     layout->num_tokens * (int64_t)layout->num_topk};
+  return EP_OK;
+}
+int dense_group(int64_t rows, ep::RowGroups* g) {
+  if (rows < 0 || rows > kInt32Limit) return EP_ERR_SHAPE;
+  *g = ep::RowGroups{nullptr, nullptr, 1, 0, rows, rows};
+  return EP_OK;
+}
+
+// Forward of ep_expert_gemm and ep_linear.
+int forward(ep::GemmArgs& g, const void* x, const void* x_scales, const void* w,
+            const void* w_scales, int32_t in_f, int32_t out_f, int32_t dtype, void* stream) {
+  const int32_t base = ep::dtype_base(dtype);
+  const bool fp8 = ep::dtype_is_fp8(base);
+  if ((base != EP_BF16 && base != EP_F16 && !fp8) || ep::dtype_read_x_ahead(dtype) || !known_act(g.act))
+    return EP_ERR_DTYPE;
+  if (ep::dtype_scales_mn(dtype) && base != EP_FP8_E4M3 && base != EP_FP8_E4M3_POW2)
+    return EP_ERR_DTYPE;
+  if (!feature_size(in_f, fp8 ? 128 : 8) || !feature_size(out_f, fp8 ? 128 : 8)) return EP_ERR_SHAPE;
+  if (g.groups.rows == 0) return EP_OK;
+  if (x == nullptr || w == nullptr || g.out == nullptr ||
+      (fp8 && (x_scales == nullptr || w_scales == nullptr)))
+    return EP_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(g.bias) || !aligned16(g.residual) ||
+      !aligned16(g.preact) || !aligned16(g.out) || (fp8 && (!aligned4(x_scales) || !aligned4(w_scales))))
+    return EP_ERR_ALIGN;
+  const int32_t width = g.act == EP_ACT_SWIGLU ? 2 * out_f : out_f;
+  g.a = x;
+  g.b = w;
+  g.lda = g.ldb = g.reduce = in_f;
+  g.out_cols = out_f;
+  g.b_stride = (int64_t)width * in_f;
+  if (fp8) {
+    const bool mn = ep::dtype_scales_mn(dtype);
+    g.a_scales = x_scales;
+    g.b_scales = w_scales;
+    g.a_scale_row = mn ? 1 : in_f / 128;
+    g.a_scale_step = mn ? g.groups.rows : 1;
+    return launch_status(ep::launch_gemm_fp8(g, base == EP_MXFP8_E4M3, static_cast<hipStream_t>(stream)));
+  }
+  return launch_status(ep::launch_gemm(g, 0, base == EP_F16, static_cast<hipStream_t>(stream)));
+}
+
+int rows_grad(ep::GemmArgs& g, const void* dy, const void* w, int32_t in_f, int32_t out_f,
+              int32_t dtype, void* stream) {
+  if ((dtype != EP_BF16 && dtype != EP_F16) || !known_act(g.act)) return EP_ERR_DTYPE;
+  if (!feature_size(in_f, 8) || !feature_size(out_f, 8)) return EP_ERR_SHAPE;
+  if (g.groups.rows == 0) return EP_OK;
+  if (dy == nullptr || w == nullptr || g.out == nullptr ||
+      (g.act != EP_ACT_NONE && g.preact == nullptr))
+    return EP_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(w) || !aligned16(g.out) ||
+      (g.act != EP_ACT_NONE && !aligned16(g.preact)))
+    return EP_ERR_ALIGN;
+  g.a = dy;
+  g.b = w;
+  g.lda = g.reduce = out_f;
+  g.ldb = g.out_cols = in_f;
+  g.b_stride = (int64_t)out_f * in_f;
+  return launch_status(ep::launch_gemm(g, 1, dtype == EP_F16, static_cast<hipStream_t>(stream)));
+}
+
+int weights_grad(ep::GemmArgs& g, const void* dy, const void* x, int32_t in_f, int32_t out_f,
+                 int32_t dtype, void* stream) {
+  const int32_t base = dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE);
+  if (base != EP_BF16 && base != EP_F16) return EP_ERR_DTYPE;
+  if (!feature_size(in_f, 8) || !feature_size(out_f, 8)) return EP_ERR_SHAPE;
+  if (g.out == nullptr || (g.groups.rows > 0 && (dy == nullptr || x == nullptr))) return EP_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(g.out) || !aligned16(g.bias_grad))
+    return EP_ERR_ALIGN;
+  g.a = dy;
+  g.b = x;
+  g.lda = g.out_rows = out_f;
+  g.ldb = g.out_cols = in_f;
+  g.grad_f32 = (dtype & EP_GRAD_F32) != 0;
+  g.accumulate = (dtype & EP_GRAD_ACCUMULATE) != 0;
+  return launch_status(ep::launch_gemm(g, 2, base == EP_F16, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -314,6 +410,112 @@ int ep_combine_groups(const void* z, const ep_layout_t* group_layout, int32_t hi
                                                  static_cast<hipStream_t>(stream)));
 }
 
+int ep_expert_gemm(const void* x, const void* x_scales, const void* weights,
+                   const void* weight_scales, const void* bias, const ep_layout_t* layout,
+                   int32_t in_features, int32_t out_features, int32_t dtype, int32_t act,
+                   void* preact, void* out, void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = layout_groups(layout, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.act = act;
+  g.bias = bias;
+  g.preact = preact;
+  g.out = out;
+  return forward(g, x, x_scales, weights, weight_scales, in_features, out_features, dtype, stream);
+}
+
+int ep_expert_gemm_grad_x(const void* dy, const void* weights, const ep_layout_t* layout,
+                          int32_t in_features, int32_t out_features, int32_t dtype, int32_t act,
+                          const void* preact, void* dx, void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = layout_groups(layout, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.act = act;
+  g.preact = const_cast<void*>(preact);
+  g.out = dx;
+  return rows_grad(g, dy, weights, in_features, out_features, dtype, stream);
+}
+
+int ep_expert_gemm_grad_w(const void* dy, const void* x, const ep_layout_t* layout,
+                          int32_t in_features, int32_t out_features, int32_t dtype,
+                          void* dweights, void* dbias, void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = layout_groups(layout, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.out = dweights;
+  g.bias_grad = dbias;
+  return weights_grad(g, dy, x, in_features, out_features, dtype, stream);
+}
+
+int ep_linear(const void* x, const void* weights, const void* bias, const void* residual,
+              int64_t rows, int32_t in_features, int32_t out_features, int32_t dtype, int32_t act,
+              void* preact, void* out, void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = dense_group(rows, &g.groups);
+  if (rc != EP_OK) return rc;
+  if (dtype != EP_BF16 && dtype != EP_F16) return EP_ERR_DTYPE;
+  g.act = act;
+  g.bias = bias;
+  g.residual = residual;
+  g.preact = preact;
+  g.out = out;
+  return forward(g, x, nullptr, weights, nullptr, in_features, out_features, dtype, stream);
+}
+
+int ep_linear_grad_x(const void* dy, const void* weights, int64_t rows, int32_t in_features,
+                     int32_t out_features, int32_t dtype, int32_t act, const void* preact,
+                     void* dx, void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = dense_group(rows, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.act = act;
+  g.preact = const_cast<void*>(preact);
+  g.out = dx;
+  return rows_grad(g, dy, weights, in_features, out_features, dtype, stream);
+}
+
+int ep_linear_grad_w(const void* dy, const void* x, int64_t rows, int32_t in_features,
+                     int32_t out_features, int32_t dtype, void* dweights, void* dbias,
+                     void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = dense_group(rows, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.out = dweights;
+  g.bias_grad = dbias;
+  return weights_grad(g, dy, x, in_features, out_features, dtype, stream);
+}
+
+int ep_act_grad(const void* dy, const void* preact, int64_t rows, int32_t n, int32_t dtype,
+                int32_t act, void* dz, void* stream) {
+  if ((dtype != EP_BF16 && dtype != EP_F16) || !known_act(act)) return EP_ERR_DTYPE;
+  if (rows < 0 || rows > kInt32Limit || !feature_size(n, 8)) return EP_ERR_SHAPE;
+  if (rows == 0) return EP_OK;
+  if (dy == nullptr || preact == nullptr || dz == nullptr) return EP_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(preact) || !aligned16(dz)) return EP_ERR_ALIGN;
+  if (act == EP_ACT_SWIGLU && dz == dy) return EP_ERR_SHAPE;
+  return launch_status(ep::launch_act_grad(dy, preact, rows, n, dtype == EP_F16, act, dz,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int ep_combine_grad(const void* dout, const void* expert_out, const float* topk_weights,
+                    const ep_layout_t* layout, int32_t hidden, int32_t dtype, void* d_expert_out,
+                    float* d_topk_weights, void* stream) {
+  const int rc = check_layout(layout);
+  if (rc != EP_OK) return rc;
+  if (dtype != EP_BF16 && dtype != EP_F16) return EP_ERR_DTYPE;
+  if (!feature_size(hidden, 8)) return EP_ERR_SHAPE;
+  if (layout->num_tokens == 0) return EP_OK;
+  if (dout == nullptr || topk_weights == nullptr || d_expert_out == nullptr ||
+      (d_topk_weights != nullptr && expert_out == nullptr))
+    return EP_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(expert_out) || !aligned16(d_expert_out) ||
+      !aligned4(topk_weights) || !aligned4(d_topk_weights))
+    return EP_ERR_ALIGN;
+  return launch_status(ep::launch_combine_grad(dout, expert_out, topk_weights, *layout, hidden,
+                                               dtype == EP_F16, d_expert_out, d_topk_weights,
+                                               static_cast<hipStream_t>(stream)));
+}
+
 int ep_dequant_fp8(const uint8_t* q, const float* scales, int64_t rows, int32_t hidden, void* y,
                    void* stream) {
   if (rows < 0 || hidden < 128 || hidden > EP_MAX_HIDDEN || hidden % 128 != 0)
@@ -379,7 +581,7 @@ const char* ep_status_string(int status) {
     case EP_ERR_ALIGN: return "a buffer is not aligned as required";
     case EP_ERR_WORKSPACE: return "workspace smaller than its size query reports";
     case EP_ERR_LAUNCH: return "the HIP runtime reported a launch error";
-    case EP_ERR_DTYPE: return "unknown receive dtype";
+    case EP_ERR_DTYPE: return "unknown receive dtype, activation or flag";
     default: return "unknown status";
   }
 }

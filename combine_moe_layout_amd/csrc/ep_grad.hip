@@ -1,0 +1,180 @@
+// ep_grad.hip -- the gradients that are not matrix products: the weighted
+// combine's, and an activation's.
+//
+// Combine: out[t] = sum_j w[t,j] y[slot[t,j]], so
+//   dy[slot[t,j]] = w[t,j] dout[t]          (rounded once)
+//   dw[t,j]       = sum_h dout[t,h] y[slot[t,j],h]   (fp32; 0 for a pair without a row)
+// Bound by HBM: dout is read once, every used row of y read once and of dy
+// written once.  One workgroup holds a token's dout row in registers, 16 bytes
+// to a lane, and walks its pairs, all of whose y rows are loaded before the
+// first is used; the dot products meet in LDS in a fixed order, so the result
+// does not depend on timing.  Small batches split a token's pairs over
+// workgroups (each reads dout, from L2) so that every CU has work.
+#include "ep_gemm.h"
+
+namespace ep {
+
+namespace {
+
+constexpr int kMaxLanes = 1024;
+constexpr int kPairsAtOnce = 8;
+
+template <bool kF16>
+__device__ __forceinline__ void unpack8(const u32x4& d, float* f) {
+  const uint32_t u[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = elem_low<kF16>(u[i]);
+    f[2 * i + 1] = elem_high<kF16>(u[i]);
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ u32x4 pack8_rne(const float* f) {
+  return u32x4{elem_rne2<kF16>(f[0], f[1]), elem_rne2<kF16>(f[2], f[3]), elem_rne2<kF16>(f[4], f[5]),
+               elem_rne2<kF16>(f[6], f[7])};
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// lanes: threads of one token (a multiple of 64); the block holds blockDim / lanes
+// tokens.  pairs: pairs of one workgroup (at most kPairsAtOnce), splits: workgroups per token.
+template <bool kF16, bool kDw>
+__global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
+    const u32x4* __restrict__ dout, const u32x4* __restrict__ y, const float* __restrict__ w,
+    const int32_t* __restrict__ slot, int64_t tokens, int32_t k, int32_t vecs, int32_t lanes,
+    int32_t pairs, int32_t splits, u32x4* __restrict__ dy, float* __restrict__ dw) {
+  __shared__ float part[kMaxLanes / 64][kPairsAtOnce];
+  const int local = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int64_t block = blockIdx.x;
+  const int64_t t = block / splits * (blockDim.x / lanes) + local;
+  const int j0 = (int)(block % splits) * pairs;
+  const int n = t < tokens ? min(pairs, k - j0) : 0;
+  int64_t row[kPairsAtOnce];
+  float weight[kPairsAtOnce], dot[kPairsAtOnce];
+#pragma unroll
+  for (int j = 0; j < kPairsAtOnce; ++j) {
+    row[j] = j < n ? (int64_t)slot[t * k + j0 + j] : -1;
+    weight[j] = j < n ? w[t * k + j0 + j] : 0.f;
+    dot[j] = 0.f;
+  }
+  if (n > 0) {
+    for (int v = lane; v < vecs; v += lanes) {
+      u32x4 rows[kPairsAtOnce];
+      if constexpr (kDw) {
+#pragma unroll
+        for (int j = 0; j < kPairsAtOnce; ++j)
+          if (row[j] >= 0) rows[j] = load_nt(y + row[j] * vecs + v);
+      }
+      float d[8];
+      unpack8<kF16>(dout[t * vecs + v], d);
+#pragma unroll
+      for (int j = 0; j < kPairsAtOnce; ++j) {
+        if (row[j] < 0) continue;
+        if constexpr (kDw) {
+          float f[8];
+          unpack8<kF16>(rows[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+        }
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = weight[j] * d[i];
+        store_nt(dy + row[j] * vecs + v, pack8_rne<kF16>(o));
+      }
+    }
+  }
+  if constexpr (kDw) {
+    const int wave = threadIdx.x >> 6, waves = lanes >> 6;
+#pragma unroll
+    for (int j = 0; j < kPairsAtOnce; ++j) {
+      const float s = wave_sum(dot[j]);
+      if ((threadIdx.x & 63) == 0) part[wave][j] = s;
+    }
+    __syncthreads();
+    if (lane < n) {
+      float s = 0.f;
+      for (int i = 0; i < waves; ++i) s += part[local * waves + i][lane];
+      dw[t * k + j0 + lane] = s;
+    }
+  }
+}
+
+// dz = dy act'(z), 8 columns to a lane; swiglu: z and dz rows are 2n wide.
+template <bool kF16>
+__global__ __launch_bounds__(256) void act_grad_kernel(const u32x4* __restrict__ dy,
+                                                       const u32x4* __restrict__ z, int64_t vecs,
+                                                       int32_t row_vecs, int32_t act,
+                                                       u32x4* __restrict__ dz) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * 256) {
+    float d[8], a[8];
+    unpack8<kF16>(dy[i], d);
+    if (act != EP_ACT_SWIGLU) {
+      unpack8<kF16>(z[i], a);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = act_backward<true>(act, d[k], a[k]);
+      dz[i] = pack8_rne<kF16>(d);
+    } else {
+      const int64_t at = i / row_vecs * row_vecs * 2 + i % row_vecs;
+      float up[8], du[8];
+      unpack8<kF16>(z[at], a);
+      unpack8<kF16>(z[at + row_vecs], up);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        du[k] = d[k] * silu<true>(a[k]);
+        d[k] = d[k] * up[k] * silu_slope<true>(a[k]);
+      }
+      dz[at] = pack8_rne<kF16>(d);
+      dz[at + row_vecs] = pack8_rne<kF16>(du);
+    }
+  }
+}
+
+template <bool kF16>
+hipError_t combine_grad(const void* dout, const void* y, const float* w, const ep_layout_t& L,
+                        int32_t hidden, void* dy, float* dw, hipStream_t stream) {
+  const int32_t vecs = hidden / 8;
+  int32_t lanes = (vecs + 63) / 64 * 64;
+  if (lanes > kMaxLanes) lanes = kMaxLanes;
+  const int32_t tokens_per_block = lanes >= 256 ? 1 : 256 / lanes;
+  const int64_t token_blocks = (L.num_tokens + tokens_per_block - 1) / tokens_per_block;
+  // At least four workgroups to a CU while there are pairs to split.
+  int32_t pairs = L.num_topk < kPairsAtOnce ? L.num_topk : kPairsAtOnce;
+  while (pairs > 1 && token_blocks * ((L.num_topk + pairs - 1) / pairs) < 4 * kChipCUs) pairs = (pairs + 1) / 2;
+  const int32_t splits = (L.num_topk + pairs - 1) / pairs;
+  const int64_t blocks = token_blocks * splits;
+  if (!grid_fits(blocks, lanes * tokens_per_block)) return hipErrorInvalidValue;
+  const auto args = [&](auto kernel) {
+    kernel<<<(uint32_t)blocks, lanes * tokens_per_block, 0, stream>>>(
+        static_cast<const u32x4*>(dout), static_cast<const u32x4*>(y), w, L.slot_idx, L.num_tokens,
+        L.num_topk, vecs, lanes, pairs, splits, static_cast<u32x4*>(dy), dw);
+  };
+  if (dw != nullptr) args(combine_grad_kernel<kF16, true>);
+  else args(combine_grad_kernel<kF16, false>);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine_grad(const void* dout, const void* y, const float* w, const ep_layout_t& L,
+                               int32_t hidden, bool f16, void* dy, float* dw, hipStream_t stream) {
+  return f16 ? combine_grad<true>(dout, y, w, L, hidden, dy, dw, stream)
+             : combine_grad<false>(dout, y, w, L, hidden, dy, dw, stream);
+}
+
+hipError_t launch_act_grad(const void* dy, const void* z, int64_t rows, int32_t n, bool f16,
+                           int32_t act, void* dz, hipStream_t stream) {
+  const int64_t vecs = rows * (n / 8);
+  const int64_t need = (vecs + 255) / 256;
+  const uint32_t blocks = (uint32_t)(need < 16 * kChipCUs ? need : 16 * kChipCUs);
+  const u32x4 *d = static_cast<const u32x4*>(dy), *a = static_cast<const u32x4*>(z);
+  u32x4* o = static_cast<u32x4*>(dz);
+  if (f16) act_grad_kernel<true><<<blocks, 256, 0, stream>>>(d, a, vecs, n / 8, act, o);
+  else act_grad_kernel<false><<<blocks, 256, 0, stream>>>(d, a, vecs, n / 8, act, o);
+  return hipGetLastError();
+}
+
+}  // namespace ep
