@@ -58,9 +58,11 @@ __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// Every LDS read of this wave has returned, then all waves of the workgroup meet.
+// Every LDS access of this wave but the kYoung youngest has returned (they
+// return in order), then all waves of the workgroup meet.
+template <int kYoung = 0>
 __device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(%0)\n\ts_barrier" ::"n"(kYoung) : "memory");
 }
 
 // --------------------------------------------------------------------------

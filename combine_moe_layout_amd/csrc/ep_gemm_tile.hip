@@ -9,26 +9,33 @@
 // e is the group (expert) that row r belongs to.  The products are summed in
 // fp32 by the matrix instructions and rounded once, after the epilogue.
 //
-// A workgroup of 4 waves makes one tile; each wave owns TM x TN blocks of 16 x
-// 16 results.  The reduction is cut into stages of 32; a ring of 4 stages in LDS is
-// filled by loads that need no registers, up to three stages ahead.  While the
-// matrix instructions work on stage s, the matrix operand of stage s + 1 and
-// the row operand's next fragments are read into registers, so one barrier a
-// stage is the only time that they can stand still.
+// A workgroup of WM x WN waves makes one tile; each wave owns TM x TN blocks of
+// 16 x 16 results.  The reduction is cut into units of 64, so that a load to LDS
+// (which needs no registers) covers rows of 128 bytes: rows of 64 bytes, in units
+// of 32, come in at 14.5 TB/s from L2 where these reach 31, and 256 x 256 tiles
+// need 19.  LDS holds three units of the row operand and two of the matrix
+// operand.  A step is half a unit, 32 deep: while the matrix instructions work on
+// step s, the matrix fragments of step s + 1 and the next row fragments are read
+// into registers, so a matrix unit is free a step earlier than a row unit, and
+// the even steps bring in the row unit two units ahead, the odd steps the matrix
+// unit.  One barrier a step is the only time that a wave stands still.
 //
 // The matrix operand takes the instruction's row side and the row operand its
 // column side, so that a lane ends up with 4 neighbouring columns of one result
 // row.  Where an operand has its reduction as the slow dimension, the
 // transposing LDS read makes the fragments.
+#include <type_traits>
+
 #include "ep_gemm.h"
 
 namespace ep {
 
 namespace {
 
-constexpr int kStage = 32;  // reduction elements per stage (64 bytes)
-constexpr int kSlots = 4;   // stages in the ring
-constexpr int kWaves = 4;
+constexpr int kStep = 32;   // reduction elements per step: one matrix instruction's
+constexpr int kUnit = 64;   // and per unit in LDS
+constexpr int kASlots = 3;  // units of the row operand in LDS
+constexpr int kBSlots = 2;  // and of the matrix operand
 
 template <bool kF16>
 struct Frag;
@@ -47,54 +54,49 @@ struct Frag<true> {
   }
 };
 
-// How `kSpan` rows (or columns) of an operand sit in a stage of LDS, and how
-// they get there.
-//  Reduction contiguous in memory: kSpan rows of 64 bytes, 16-byte chunk c of
-//  row r at place c ^ ((r >> 2) & 3), so that the 16 lanes that read one chunk
-//  of 16 neighbouring rows touch every bank once.
-//  Reduction slow in memory: 32 rows of kSpan elements, pair p of 16-byte
-//  chunks of row k at place p ^ f(k), f(k) = 4 * bit 3 of k + (k & 3): the
-//  eight rows that one half wave of a transposing read touches lie in
-//  different banks.
-template <bool kContiguous, int kSpan>
+// How `kSpan` rows (or columns) of an operand sit in a unit of LDS, and how they
+// get there.
+//  Reduction contiguous in memory: kSpan rows of 128 bytes, 16-byte chunk c of
+//  row r at place c ^ ((r >> 1) & 7).  A 16-byte read goes in four phases of 16
+//  lanes, 0-3, 12-15, 20-23, 24-27 and so on; with this order the lanes of a
+//  phase touch every bank once.
+//  Reduction slow in memory: 64 rows of kSpan elements, pair p of 16-byte chunks
+//  of row k at place p ^ f(k), f(k) = 4 * bit 3 of k + (k & 3): the eight rows
+//  that one half wave of a transposing read touches lie in different banks.
+template <bool kContiguous, int kSpan, int kWaves>
 struct Operand {
-  static constexpr int kBytes = kSpan * kStage * 2;
-  static constexpr int kLoads = kBytes / 1024 / kWaves;  // loads of a wave per stage
-  static constexpr int kChunks = kSpan / 8;              // chunks per LDS row, slow reduction
+  static constexpr int kBytes = kSpan * kUnit * 2;
+  static constexpr int kLoads = kBytes / 1024 / kWaves;  // loads of a wave per unit
+  static constexpr int kChunks = kContiguous ? 8 : kSpan / 8;  // chunks per LDS row
   static_assert(kContiguous || kSpan >= 128, "the bank pattern spans 16 chunks");
 
   static __device__ __forceinline__ int swizzle(int k) { return ((k >> 3) & 1) * 4 + (k & 3); }
 
   // The row (contiguous) or reduction row (slow) of this lane's i-th load, and its chunk.
   static __device__ __forceinline__ int load_row(int i) {
-    const int j = (threadIdx.x >> 6) * kLoads + i, lane = threadIdx.x & 63;
-    return kContiguous ? j * 16 + (lane >> 2) : j * (64 / kChunks) + lane / kChunks;
+    return ((threadIdx.x >> 6) * kLoads + i) * (64 / kChunks) + (threadIdx.x & 63) / kChunks;
   }
   static __device__ __forceinline__ int load_chunk(int i) {
-    const int lane = threadIdx.x & 63, row = load_row(i);
-    return kContiguous ? ((lane & 3) ^ ((row >> 2) & 3))
-                       : ((lane % kChunks) ^ (swizzle(row) << 1));
-  }
-  static __device__ __forceinline__ uint32_t load_place(int i) {  // the wave's LDS offset
-    return ((threadIdx.x >> 6) * kLoads + i) * 1024;
+    const int place = (threadIdx.x & 63) % kChunks, row = load_row(i);
+    return kContiguous ? (place ^ ((row >> 1) & 7)) : (place ^ (swizzle(row) << 1));
   }
 };
 
 template <int kMode, bool kF16, bool kGlu, int TM, int TN, int WM, int WN>
 struct TileGemm {
-  static_assert(WM * WN == kWaves, "four waves");
+  static constexpr int kWaves = WM * WN;
   static constexpr int kRows = 16 * TM * WM;  // result rows of a tile
   static constexpr int kCols = 16 * TN * WN;  // product columns of a tile
   static constexpr bool kAContig = kMode != kWeightsGrad;
   static constexpr bool kBContig = kMode == kForward;
-  typedef Operand<kAContig, kRows> A;
-  typedef Operand<kBContig, kCols> B;
+  typedef Operand<kAContig, kRows, kWaves> A;
+  typedef Operand<kBContig, kCols, kWaves> B;
   typedef typename Frag<kF16>::type F;
-  static constexpr int kStageBytes = A::kBytes + B::kBytes;
-  static constexpr int kLoads = A::kLoads + B::kLoads;
-  static constexpr int kAhead = 3;  // row fragments read ahead of their use
+  static constexpr int kLdsBytes = kASlots * A::kBytes + kBSlots * B::kBytes;
+  static constexpr int kAhead = TM == 8 ? 4 : 2;  // row fragments read ahead
+  static constexpr int kRing = TM == 8 ? 8 : 4;   // at least kAhead + 2: a pair is in use meanwhile
   static constexpr int kWaveCols = 16 * TN;
-  static constexpr int kWaveBytes = kSlots * kStageBytes / kWaves;
+  static constexpr int kWaveBytes = kLdsBytes / kWaves / 1024 * 1024;
   typedef TileStore<kMode, kF16, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
 
@@ -102,18 +104,19 @@ struct TileGemm {
   char* const lds;
   uint32_t lds0;
   Tile t;
-  int32_t reduce, stages, whole_stages;
+  int32_t reduce, units, whole_units;
   int32_t a_limit, b_limit;  // valid rows (contiguous) or columns (slow) of each operand
   const char *a0, *b0;       // first element of the operand of this tile
-  int64_t a_step, b_step;    // bytes from one stage to the next
+  int64_t a_step, b_step;    // bytes from one unit to the next
   uint32_t a_off[A::kLoads], b_off[B::kLoads];
   uint32_t a_read, b_read;
+  uint32_t a_place, b_place;  // where a wave's loads go in slot 0
   int wm, wn, lane;
   int blocks;  // blocks of 16 rows of this wave that the tile has
   f32x4 acc[TM][TN];
   float bias_sum[2];
   bool bias_tile;
-  F af[kAhead + 1], bf[2][TN];
+  F af[kRing], bf[2][TN];
 
   __device__ __forceinline__ TileGemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
@@ -135,10 +138,12 @@ struct TileGemm {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
     wn = wave % WN;
-    lds0 = lds_address(lds);
-    blocks = ((t.rows + 15) / 16 - wm + WM - 1) / WM;
-    whole_stages = reduce / kStage;
-    stages = (reduce + 2 * kStage - 1) / (2 * kStage) * 2;  // an even number: the last may be all zeros
+    lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
+    blocks = __builtin_amdgcn_readfirstlane(((t.rows + 15) / 16 - wm + WM - 1) / WM);
+    a_place = lds0 + wave * A::kLoads * 1024;
+    b_place = lds0 + kASlots * A::kBytes + wave * B::kLoads * 1024;
+    whole_units = reduce / kUnit;
+    units = (reduce + kUnit - 1) / kUnit;
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int row = A::load_row(i), chunk = A::load_chunk(i);
@@ -151,10 +156,10 @@ struct TileGemm {
       if constexpr (kBContig) b_off[i] = (uint32_t)matrix_row(row) * (uint32_t)g.ldb * 2u + chunk * 16;
       else b_off[i] = (uint32_t)row * (uint32_t)g.ldb * 2u + min(chunk * 8, b_limit - 8) * 2;
     }
-    a_step = kAContig ? kStage * 2 : (int64_t)kStage * g.lda * 2;
-    b_step = kBContig ? kStage * 2 : (int64_t)kStage * g.ldb * 2;
+    a_step = kAContig ? kUnit * 2 : (int64_t)kUnit * g.lda * 2;
+    b_step = kBContig ? kUnit * 2 : (int64_t)kUnit * g.ldb * 2;
     a_read = read_offset<A, kAContig>(wm * 16);
-    b_read = A::kBytes + read_offset<B, kBContig>(wn * 16 * TN);
+    b_read = kASlots * A::kBytes + read_offset<B, kBContig>(wn * 16 * TN);
   }
 
   // LDS offset of this lane's part of the first fragment at row (column) w0.
@@ -162,7 +167,7 @@ struct TileGemm {
   __device__ __forceinline__ uint32_t read_offset(int w0) const {
     const int q = lane >> 4, m = lane & 15;
     if constexpr (kContig) {
-      return (w0 + m) * 64 + ((q ^ ((m >> 2) & 3)) << 4);
+      return (w0 + m) * 128 + ((q ^ ((m >> 1) & 7)) << 4);
     } else {
       const int k = q * 8 + (m >> 2), gran = m & 3;
       return k * (Op::kChunks * 16) + (((w0 >> 3) ^ (Op::swizzle(k) << 1)) << 4) + ((gran >> 1) << 4) +
@@ -170,16 +175,17 @@ struct TileGemm {
     }
   }
 
-  // A wave's blocks of the row operand are every WM-th one of the tile, so that a
-  // tile with few rows is shared by all waves; those of the other operand are
+  // Fragment `tile` of half `kHalf` of the unit at LDS offset `unit`.  A wave's
+  // blocks of the row operand are every WM-th one of the tile, so that a tile
+  // with few rows is shared by all waves; those of the other operand are
   // neighbours.
-  template <class Op, bool kContig>
+  template <class Op, bool kContig, int kHalf>
   __device__ __forceinline__ F read_fragment(uint32_t offset, int tile) const {
     if constexpr (kContig) {
-      return *reinterpret_cast<const F*>(lds + offset + tile * 1024);
+      return *reinterpret_cast<const F*>(lds + (offset ^ (kHalf * 64)) + tile * 2048);
     } else {
       // Two transposing reads: reduction rows q*8 .. q*8+3, and the four after them.
-      const uint32_t at = offset ^ (uint32_t)(tile << 5);
+      const uint32_t at = (offset ^ (uint32_t)(tile << 5)) + kHalf * kStep * Op::kChunks * 16;
       typedef __attribute__((address_space(3))) s16x4 lds4;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)(lds0 + at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -187,97 +193,149 @@ struct TileGemm {
       return __builtin_bit_cast(F, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
-
-  // Load j of a whole stage (the first A::kLoads are the row operand's).
-  __device__ __forceinline__ void load_piece(int s, uint32_t slot, int j) const {
-    const uint32_t at = lds0 + slot * kStageBytes;
-    if (j < A::kLoads)
-      load16_to_lds(a0 + s * a_step, a_off[j < A::kLoads ? j : 0],
-                    __builtin_amdgcn_readfirstlane(at + A::load_place(j)));
-    else
-      load16_to_lds(b0 + s * b_step, b_off[j < A::kLoads ? 0 : j - A::kLoads],
-                    __builtin_amdgcn_readfirstlane(at + A::kBytes + B::load_place(j - A::kLoads)));
+  template <int kHalf>
+  __device__ __forceinline__ F read_a(uint32_t unit, int i) const {
+    return read_fragment<A, kAContig, kHalf>(unit + a_read, i * WM);
   }
-  // All loads of a stage; what lies past the reduction reads as zero.
-  __device__ __forceinline__ void load_stage(int s, uint32_t slot) const {
-    const int left = reduce - s * kStage;
-    if (left >= kStage) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) load_piece(s, slot, j);
-      return;
-    }
-    const uint32_t at = lds0 + slot * kStageBytes;
-#pragma unroll
-    for (int i = 0; i < A::kLoads; ++i) {
-      const int r = kAContig ? A::load_chunk(i) * 8 : A::load_row(i);
-      const char* p = r < left ? a0 + s * a_step + a_off[i] : reinterpret_cast<const char*>(g_zero16);
-      load16_to_lds(p, __builtin_amdgcn_readfirstlane(at + A::load_place(i)));
-    }
-#pragma unroll
-    for (int i = 0; i < B::kLoads; ++i) {
-      const int r = kBContig ? B::load_chunk(i) * 8 : B::load_row(i);
-      const char* p = r < left ? b0 + s * b_step + b_off[i] : reinterpret_cast<const char*>(g_zero16);
-      load16_to_lds(p, __builtin_amdgcn_readfirstlane(at + A::kBytes + B::load_place(i)));
-    }
+  template <int kHalf>
+  __device__ __forceinline__ F read_b(uint32_t unit, int j) const {
+    return read_fragment<B, kBContig, kHalf>(unit + b_read, j);
   }
 
-  // Stage s.  Its matrix fragments are in the registers of `kSet` and its first
-  // kAhead row fragments in af; the other row fragments are read while the
-  // matrix instructions work, and so are the next stage's first ones.
-  template <int kSet>
-  __device__ __forceinline__ void step(int s) {
-    // Stage s + 1 has landed, for every wave; and every wave is done with stage s - 1.
-    if (s + 2 < stages) wait_loads<(kSlots - 3) * kLoads>();
-    else wait_loads<0>();
-    lds_barrier();
-    const int ahead = s + kSlots - 1;
-    const uint32_t slot = ahead % kSlots;
-    const uint32_t base = (s % kSlots) * kStageBytes, next = ((s + 1) % kSlots) * kStageBytes;
-    const bool whole = ahead < whole_stages;
-    if (!whole && ahead < stages) load_stage(ahead, slot);
-    if constexpr (kMode == kWeightsGrad) {
-      if (bias_tile) add_to_bias(base);
-    }
+  // Load j of unit u of one operand, into the slot at LDS offset `slot` (of that
+  // operand); whole: nothing of it lies past the reduction.
+  template <bool kA>
+  __device__ __forceinline__ void load_piece(const char* unit, uint32_t slot, int j) const {
+    if constexpr (kA) load16_to_lds(unit, a_off[j], a_place + slot + j * 1024);
+    else load16_to_lds(unit, b_off[j], b_place + slot + j * 1024);
+  }
+  // All loads of a unit; what lies past the reduction reads as zero.
+  template <bool kA>
+  __device__ __forceinline__ void load_unit(int u, uint32_t slot) const {
+    typedef std::conditional_t<kA, A, B> Op;
+    const int left = reduce - u * kUnit;
+    const char* unit = kA ? a0 + u * a_step : b0 + u * b_step;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        if (j * TM / kLoads == i && whole) load_piece(ahead, slot, j);
-      // (past the last stage these read a slot whose contents nobody uses)
-      constexpr int kRing = kAhead + 1;
-      static_assert(2 * TM % kRing == 0, "two steps leave the ring where it was");
-      const int f = i + kAhead;
-      af[(kSet * TM + f) % kRing] = f < TM ? read_fragment<A, kAContig>(base + a_read, f * WM)
-                                           : read_fragment<A, kAContig>(next + a_read, (f - TM) * WM);
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        if (j * TM / TN == i) bf[1 - kSet][j] = read_fragment<B, kBContig>(next + b_read, j);
-      const F a = af[(kSet * TM + i) % kRing];
-      if (i < blocks) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = Frag<kF16>::mfma(bf[kSet][j], a, acc[i][j]);
+    for (int i = 0; i < Op::kLoads; ++i) {
+      if (left >= kUnit) {
+        load_piece<kA>(unit, slot, i);
+      } else {
+        const int r = (kA ? kAContig : kBContig) ? Op::load_chunk(i) * 8 : Op::load_row(i);
+        const uint32_t off = kA ? a_off[kA ? i : 0] : b_off[kA ? 0 : i];
+        load16_to_lds(r < left ? unit + off : reinterpret_cast<const char*>(g_zero16),
+                      (kA ? a_place : b_place) + slot + i * 1024);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
+
+  // Where things are in LDS while unit u is worked on: its row unit and the next
+  // one, its matrix unit and the next one, and the row slot that is free.
+  struct Slots {
+    uint32_t a, a_next, a_free, b, b_next;
+    __device__ __forceinline__ void turn() {
+      const uint32_t free = a;
+      a = a_next;
+      a_next = a_free;
+      a_free = free;
+      const uint32_t last = b;
+      b = b_next;
+      b_next = last;
+    }
+  };
+
+  // Step kHalf of unit u.  Its matrix fragments are in bf[kHalf] and its first
+  // kAhead row fragments in af; the other row fragments are read while the
+  // matrix instructions work, and so are the next step's first ones.
+  template <int kHalf>
+  __device__ __forceinline__ void step(int u, const Slots& at) {
+    static_assert(TM % kRing == 0, "a step leaves the ring where it was");
+    // Half 0: every wave is done with the row unit u - 1.  Half 1: unit u + 1 has
+    // landed, for every wave (of later loads only the row unit u + 2 may be on
+    // its way), and every wave is done with the matrix unit u.  All but the
+    // youngest LDS reads, which are of units still in use, have returned.
+    if constexpr (kHalf == 1) {
+      if (u + 2 < units) wait_loads<A::kLoads>();
+      else wait_loads<0>();
+    }
+    lds_barrier<kYoung>();
+    const char* ahead = kHalf == 0 ? a0 + (u + 2) * a_step : b0 + (u + 2) * b_step;
+    const uint32_t slot = kHalf == 0 ? at.a_free : at.b;
+    const bool whole = u + 2 < whole_units;
+    if (!whole && u + 2 < units) load_unit<kHalf == 0>(u + 2, slot);
+    if constexpr (kMode == kWeightsGrad) {
+      if (bias_tile) add_to_bias<kHalf>(at.a);
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += 2) {
+      if (i0 < blocks) {
+        // Two matrix instructions, then one of the other operations, and so on.
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+#pragma unroll
+          for (int m = 2 * n; m < 2 * n + 2; ++m)
+            acc[i0 + m / TN][m % TN] =
+                Frag<kF16>::mfma(bf[kHalf][m % TN], af[(i0 + m / TN) % kRing], acc[i0 + m / TN][m % TN]);
+          for (int o = n; o < others<kHalf>(i0); o += TN) other_operation<kHalf>(i0, o, at, whole, ahead, slot);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < others<kHalf>(i0); ++n) other_operation<kHalf>(i0, n, at, whole, ahead, slot);
+      }
+    }
+  }
+  // What goes with the rows i0 and i0 + 1: two reads of row fragments, kPieces
+  // loads of a later unit, and in the first rows, before the reads of row
+  // fragments turn to the next step's, kBReads reads of matrix fragments.
+  static constexpr int kBReads = 2 * TN / (TM - kAhead);
+  template <int kHalf>
+  static constexpr int kLoadsOf = kHalf == 0 ? A::kLoads : B::kLoads;
+  template <int kHalf>
+  static constexpr int kPieces = (2 * kLoadsOf<kHalf> + TM - 1) / TM;
+  template <int kHalf>
+  static constexpr int others(int i0) {
+    return 2 + kPieces<kHalf> + (i0 < TM - kAhead ? kBReads : 0);
+  }
+  template <int kHalf>
+  __device__ __forceinline__ void other_operation(int i0, int n, const Slots& at, bool whole,
+                                                  const char* ahead, uint32_t slot) {
+    static_assert(kBReads * (TM - kAhead) == 2 * TN, "every matrix fragment has its turn");
+    // (past the last unit these read a slot whose contents nobody uses)
+    if (n < 2) {
+      const int f = i0 + kAhead + n;
+      af[f % kRing] = f < TM ? read_a<kHalf>(at.a, f)
+                             : read_a<1 - kHalf>(kHalf == 0 ? at.a : at.a_next, f - TM);
+    } else if (n < 2 + kPieces<kHalf>) {
+      const int j = i0 / 2 * kPieces<kHalf> + n - 2;
+      if (whole && j < kLoadsOf<kHalf>) load_piece<kHalf == 0>(ahead, slot, j);
+    } else {
+      const int j = i0 / 2 * kBReads + n - 2 - kPieces<kHalf>;
+      bf[1 - kHalf][j] = read_b<1 - kHalf>(kHalf == 0 ? at.b : at.b_next, j);
+    }
+  }
+  // The youngest LDS reads of a step, of the next step's row fragments: they come
+  // after its last reads of its own row unit's half and of the matrix unit.
+  static constexpr int kYoung = kAhead * (kAContig ? 1 : 2);
+  static_assert(kYoung < 16, "lgkmcnt holds 4 bits");
 
   // Biases' gradient: the workgroups of the first column tile add up the rows of
   // dy that pass through their LDS, two columns and a part of the stage's rows
   // to a thread.
   static constexpr int kBiasParts = kWaves * 64 / (kRows / 2);
-  __device__ __forceinline__ void add_to_bias(uint32_t base) {
+  template <int kHalf>
+  __device__ __forceinline__ void add_to_bias(uint32_t unit) {
     const int pair = threadIdx.x % (kRows / 2), part = threadIdx.x / (kRows / 2);
 #pragma unroll
-    for (int j = 0; j < kStage / kBiasParts; ++j) {
-      const int k = part * (kStage / kBiasParts) + j;
-      const uint32_t at = base + k * (A::kChunks * 16) + (((pair >> 2) ^ (A::swizzle(k) << 1)) << 4) +
+    for (int j = 0; j < kStep / kBiasParts; ++j) {
+      const int k = kHalf * kStep + part * (kStep / kBiasParts) + j;
+      const uint32_t at = unit + k * (A::kChunks * 16) + (((pair >> 2) ^ (A::swizzle(k) << 1)) << 4) +
                           (pair & 3) * 4;
       const uint32_t w = *reinterpret_cast<const uint32_t*>(lds + at);
       bias_sum[0] += elem_low<kF16>(w);
       bias_sum[1] += elem_high<kF16>(w);
     }
   }
-  // Called by all threads once the ring is free; the parts meet in LDS.
+  // Called by all threads once the operands' LDS is free; the parts meet there.
   __device__ __forceinline__ void store_bias() {
     float* sums = reinterpret_cast<float*>(lds);
     sums[threadIdx.x * 2] = bias_sum[0];
@@ -305,17 +363,26 @@ struct TileGemm {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     bias_sum[0] = bias_sum[1] = 0.f;
-    if (stages == 0) return;
-    for (int s = 0; s < kSlots - 1 && s < stages; ++s) load_stage(s, s);
-    wait_loads<0>();
+    if (units == 0) return;
+    load_unit<true>(0, 0);
+    load_unit<false>(0, 0);
+    if (units > 1) {
+      load_unit<true>(1, A::kBytes);
+      load_unit<false>(1, B::kBytes);
+      wait_loads<A::kLoads + B::kLoads>();
+    } else {
+      wait_loads<0>();
+    }
     lds_barrier();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) af[i] = read_fragment<A, kAContig>(a_read, i * WM);
+    for (int i = 0; i < kAhead; ++i) af[i] = read_a<0>(0, i);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) bf[0][j] = read_fragment<B, kBContig>(b_read, j);
-    for (int s = 0; s < stages; s += 2) {
-      step<0>(s);
-      step<1>(s + 1);
+    for (int j = 0; j < TN; ++j) bf[0][j] = read_b<0>(0, j);
+    Slots at = {0, A::kBytes, 2 * A::kBytes, 0, B::kBytes};
+    for (int u = 0; u < units; ++u) {
+      step<0>(u, at);
+      step<1>(u, at);
+      at.turn();
     }
   }
 
@@ -362,7 +429,7 @@ struct TileGemm {
     if (!place()) return;
     setup();
     accumulate();
-    lds_barrier();  // every wave is done with the ring
+    lds_barrier();  // every wave is done with its operands
     if constexpr (kMode == kWeightsGrad) {
       if (bias_tile) store_bias();
     }
@@ -371,9 +438,9 @@ struct TileGemm {
 };
 
 template <int kMode, bool kF16, bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM * TN >= 64 ? 1 : 2) void gemm_tile_kernel(GemmArgs g) {
+__global__ __launch_bounds__(WM * WN * 64, TM * TN >= 64 ? 1 : 2) void gemm_tile_kernel(GemmArgs g) {
   typedef TileGemm<kMode, kF16, kGlu, TM, TN, WM, WN> G;
-  __shared__ __align__(1024) char lds[kSlots * G::kStageBytes];
+  __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
   gemm.run();
 }
@@ -388,16 +455,16 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
   const int64_t rounds = kMode == kWeightsGrad ? (rt / g.groups.E * ct + kXcds - 1) / kXcds * g.groups.E
                                                : (rt * ct + kXcds - 1) / kXcds;
   const int64_t blocks = rounds * kXcds;
-  if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
+  if (!grid_fits(blocks, WM * WN * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
   gemm_tile_kernel<kMode, kF16, kGlu, TM, TN, WM, WN>
-      <<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g);
+      <<<(uint32_t)blocks, WM * WN * 64, 0, stream>>>(g);
   return hipGetLastError();
 }
 
 template <int kMode, bool kF16, bool kGlu>
 hipError_t launch_size(const GemmArgs& g, bool large, hipStream_t stream) {
-  return large ? launch<kMode, kF16, kGlu, 8, 8, 2, 2>(g, stream)
+  return large ? launch<kMode, kF16, kGlu, 8, 4, 2, 4>(g, stream)
                : launch<kMode, kF16, kGlu, 4, 4, 2, 2>(g, stream);
 }
 
