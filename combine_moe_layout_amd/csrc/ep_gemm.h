@@ -109,6 +109,10 @@ struct Tile {
 // skips a tile's blocks of 16 rows that it does not have).
 // Every wave does the search by itself: its lanes hold E/64 groups each.
 constexpr int kXcds = 8;
+__device__ __forceinline__ int64_t uniform(int64_t v) {  // the same in every lane: to scalar registers
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(v >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)v));
+}
 template <int kBand>
 __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, int32_t col_tiles,
                                           uint32_t block, Tile& t) {
@@ -153,6 +157,8 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   t.rows = min(each, count - left * each);
   t.row0 = group_first(g, t.e) + (int64_t)left * each;
   t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  t.row0 = uniform(t.row0);
+  t.col = __builtin_amdgcn_readfirstlane(t.col);
   return t.rows > 0;
 }
 

@@ -14,49 +14,55 @@
 // codes themselves are off by up to 2^-4 and the result is rounded to 2^-8, and
 // it is the price of the instructions that work at twice the 16-bit rate.
 //
-// A workgroup of 4 waves makes a 256 x 256 tile, 128 x 128 to a wave.  A stage
-// is 128 channels: 64 KB of codes, so two of them fit LDS.  While the matrix
-// instructions work on stage s, stage s + 1 comes in; three quarters of the way
-// it has landed and its matrix fragments go to registers, so that the next
-// stage starts without waiting for LDS.
+// A workgroup of 8 waves makes a 256 x 256 tile, 128 x 64 to a wave (with fp32
+// scales the sums pass through vector instructions, so a wave must hold them in
+// vector registers).  A stage is 128 channels: 64 KB of codes, so two of them fit
+// LDS.  While the matrix instructions work on stage s, the row operand of stage
+// s + 1 and then the matrix operand of stage s + 2 come in (the matrix operand of
+// stage s has been in registers since stage s - 1 ended, so its slot is free).
+// Three quarters of the way stage s + 1 has landed and its matrix fragments go to
+// registers, so that it starts without waiting for LDS.
 #include "ep_gemm.h"
 
 namespace ep {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kSlots = 2;
 constexpr int kStage = 128;  // channels, and bytes, per stage
 
 template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
 struct Fp8Gemm {
-  static_assert(WM * WN == kWaves, "four waves");
+  static_assert(WM * WN == kWaves, "eight waves");
   static constexpr int kRows = 16 * TM * WM, kCols = 16 * TN * WN, kWaveCols = 16 * TN;
   static constexpr int kABytes = kRows * kStage, kBBytes = kCols * kStage;
   static constexpr int kScaleBytes = (kRows + kCols) * 4;  // one word per row of both operands
-  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
+  static constexpr int kBAt = kSlots * kABytes, kScalesAt = kBAt + kSlots * kBBytes;
+  static constexpr int kLdsBytes = kScalesAt + kSlots * kScaleBytes;
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
-  static constexpr int kCodeLoads = kALoads + kBLoads;
-  static constexpr int kWaveBytes = kSlots * (kABytes + kBBytes) / kWaves;
+  static_assert(kBLoads == 4 && kWaveCols % 64 == 0, "a wave loads half of a wave's columns");
+  static_assert(kRows == 256 && kCols == 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
+  static constexpr int kWaveBytes = kScalesAt / kWaves;
   typedef TileStore<kForward, false, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
-  static constexpr int kTurn = TM * 3 / 4;  // the row of blocks before which stage s + 1 has landed
+  static constexpr int kTurn = TM - 2;  // the row of blocks before which stage s + 1 has landed
 
   const GemmArgs& g;
   char* const lds;
   uint32_t lds0;
   Tile t;
   int32_t stages, blocks;
-  const char *a0, *b0, *as0, *bs0;
-  int64_t as_step;
-  uint32_t a_off[kALoads], b_off[kBLoads], as_off, bs_off;
+  const char *a0, *b0, *s0, *bs0;
+  int64_t s_step;
+  uint32_t a_off[kALoads], b_off[2], s_off;
   uint32_t a_read, b_read, as_read, bs_read;
+  uint32_t block0, block1;  // fp32 scales: index of the wave's first block, of its ups'
   int wm, wn, lane, wave;
   f32x4 acc[TM][TN];
-  i32x8 af[2], bf[2][TN];
-  float b_scale[2][2];  // fp32 scales of the wave's columns: gates (or all), ups
-  int32_t b_byte[2][kMx ? TN : 1];
+  i32x8 af[2], bf[TN];
+  float b_scale[2];  // fp32 scales of the wave's columns: gates (or all), ups
+  int32_t b_byte[kMx ? TN : 1];
 
   __device__ __forceinline__ Fp8Gemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
@@ -77,9 +83,9 @@ struct Fp8Gemm {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
     wn = wave % WN;
-    lds0 = lds_address(lds);
+    lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
     stages = g.reduce / kStage;
-    blocks = ((t.rows + 15) / 16 - wm + WM - 1) / WM;
+    blocks = __builtin_amdgcn_readfirstlane(((t.rows + 15) / 16 - wm + WM - 1) / WM);
     a0 = static_cast<const char*>(g.a) + t.row0 * g.lda;
     b0 = static_cast<const char*>(g.b) + t.e * g.b_stride;
     // Codes: a load brings 8 rows of 128 bytes; 16-byte chunk c of row r lies at
@@ -89,52 +95,49 @@ struct Fp8Gemm {
       const int row = (wave * kALoads + i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
       a_off[i] = (uint32_t)min(row, t.rows - 1) * (uint32_t)g.lda + chunk * 16;
     }
-#pragma unroll
-    for (int i = 0; i < kBLoads; ++i) {
-      const int row = (wave * kBLoads + i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-      b_off[i] = (uint32_t)matrix_row(row) * (uint32_t)g.ldb + chunk * 16;
-    }
+    // (a wave's 32 rows of the matrix operand are neighbours in memory too: of 32
+    // rows all exist or none, as the columns are a multiple of 128)
+    const int row = wave * kBLoads * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+    b_off[0] = (uint32_t)matrix_row(row) * (uint32_t)g.ldb + chunk * 16;
+    b_off[1] = b_off[0] ^ 64;
     const int q = lane >> 4, m = lane & 15;
     const uint32_t in_row = m * kStage + ((q ^ ((m >> 1) & 7)) << 4);
     a_read = wm * 16 * kStage + in_row;
-    b_read = kABytes + wn * kWaveCols * kStage + in_row;
-    // Scale words: thread p of the workgroup brings row p's of each operand.
-    const int p = threadIdx.x;
-    as0 = static_cast<const char*>(g.a_scales) + t.row0 * g.a_scale_row * 4;
-    as_step = g.a_scale_step * 4;
-    as_off = (uint32_t)(min(p, t.rows - 1) * g.a_scale_row * 4);
-    as_read = kABytes + kBBytes + (wm * 16 + m) * 4 + (kMx ? q : 0);
-    if constexpr (kMx) {
-      bs0 = static_cast<const char*>(g.b_scales) + t.e * (g.b_stride / 32);
-      bs_off = (uint32_t)matrix_row(p) * (uint32_t)(g.ldb / 32);
-      bs_read = kABytes + kBBytes + kRows * 4 + (wn * kWaveCols + m) * 4 + q;
+    b_read = kBAt + wn * kWaveCols * kStage + in_row;
+    // Scale words: thread p brings row p's of the row operand; with E8M0 scales
+    // thread 256 + p brings row p's of the matrix operand.
+    const int p = threadIdx.x & 255;
+    bs0 = static_cast<const char*>(g.b_scales) + t.e * (kMx ? g.b_stride / 32 : g.b_stride / (128 * 128) * 4);
+    if (kMx && wave >= 4) {
+      s0 = bs0;
+      s_step = 4;
+      s_off = (uint32_t)matrix_row(p) * (uint32_t)(g.ldb / 32);
     } else {
-      // The wave's columns (64 gates and 64 ups, or 128) lie in one block of 128 each.
-      const int64_t per_row = g.ldb / 128;
-      bs0 = static_cast<const char*>(g.b_scales) + t.e * (g.b_stride / (128 * 128)) * 4;
-      bs_off = (uint32_t)(matrix_row(wn * kWaveCols) / 128 * per_row);
-      bs_read = (uint32_t)(matrix_row(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
+      s0 = static_cast<const char*>(g.a_scales) + t.row0 * g.a_scale_row * 4;
+      s_step = g.a_scale_step * 4;
+      s_off = (uint32_t)(min(p, t.rows - 1) * g.a_scale_row * 4);
     }
+    as_read = kScalesAt + (wm * 16 + m) * 4 + (kMx ? q : 0);
+    bs_read = kScalesAt + kRows * 4 + (wn * kWaveCols + m) * 4 + q;
+    // The wave's columns (32 gates and 32 ups, or 64) lie in one block of 128 each.
+    const int64_t per_row = g.ldb / 128;
+    block0 = (uint32_t)(matrix_row(wn * kWaveCols) / 128 * per_row);
+    block1 = (uint32_t)(matrix_row(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
   }
 
-  static constexpr int kLoads = kCodeLoads + 2;
-  __device__ __forceinline__ void load_piece(int s, uint32_t slot, int j) const {
-    const uint32_t at = lds0 + slot * kStageBytes;
-    if (j < kALoads) {
+  // Loads of the row operand and of the scales of stage s, and of the matrix operand.
+  static constexpr int kFirstLoads = kALoads + 1, kLoads = kFirstLoads + kBLoads;
+  __device__ __forceinline__ void load_first(int s, int j) const {
+    const uint32_t slot = s & 1;
+    if (j < kALoads)
       load16_to_lds(a0 + s * kStage, a_off[j < kALoads ? j : 0],
-                    __builtin_amdgcn_readfirstlane(at + (wave * kALoads + j) * 1024));
-    } else if (j < kCodeLoads) {
-      load16_to_lds(b0 + s * kStage, b_off[j >= kALoads && j < kCodeLoads ? j - kALoads : 0],
-                    __builtin_amdgcn_readfirstlane(at + kABytes + (wave * kBLoads + j - kALoads) * 1024));
-    } else if (j == kCodeLoads) {
-      if (kRows >= kWaves * 64 || wave < kRows / 64)
-        load4_to_lds(as0 + s * as_step, as_off,
-                     __builtin_amdgcn_readfirstlane(at + kABytes + kBBytes + wave * 256));
-    } else if constexpr (kMx) {
-      if (kCols >= kWaves * 64 || wave < kCols / 64)
-        load4_to_lds(bs0 + s * 4, bs_off,
-                     __builtin_amdgcn_readfirstlane(at + kABytes + kBBytes + kRows * 4 + wave * 256));
-    }
+                    lds0 + slot * kABytes + (wave * kALoads + j) * 1024);
+    else
+      load4_to_lds(s0 + s * s_step, s_off,
+                   lds0 + kScalesAt + slot * kScaleBytes + (kMx ? wave : wave & 3) * 256);
+  }
+  __device__ __forceinline__ void load_matrix(int s, int j) const {
+    load16_to_lds(b0 + s * kStage + (int64_t)j * 8 * g.ldb, b_off[j & 1], lds0 + kBAt + (s & 1) * kBBytes + (wave * kBLoads + j) * 1024);
   }
 
   // Lane 16 q + m holds channels 16 q .. 16 q + 15 and 64 + 16 q .. of row m
@@ -145,14 +148,13 @@ struct Fp8Gemm {
     const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + (offset ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
-  __device__ __forceinline__ i32x8 row_fragment(uint32_t base, int i) const {
-    return read_fragment(base + a_read + i * (WM * 16 * kStage));
+  __device__ __forceinline__ i32x8 row_fragment(uint32_t slot, int i) const {
+    return read_fragment(slot * kABytes + a_read + i * (WM * 16 * kStage));
   }
-  template <int kSet>
-  __device__ __forceinline__ void read_matrix(uint32_t base, int j) {
-    bf[kSet][j] = read_fragment(base + b_read + j * (16 * kStage));
+  __device__ __forceinline__ void read_matrix(uint32_t slot, int j) {
+    bf[j] = read_fragment(slot * kBBytes + b_read + j * (16 * kStage));
     if constexpr (kMx)
-      b_byte[kSet][j] = *reinterpret_cast<const uint8_t*>(lds + base + bs_read + j * 64);
+      b_byte[j] = *reinterpret_cast<const uint8_t*>(lds + slot * kScaleBytes + bs_read + j * 64);
   }
   // A block's fp32 scale, by a scalar load (it must not wait for the loads to LDS).
   __device__ __forceinline__ float block_scale(uint32_t index, int s) const {
@@ -160,57 +162,90 @@ struct Fp8Gemm {
     return ((cfloat*)(uintptr_t)bs0)[__builtin_amdgcn_readfirstlane(index) + s];
   }
 
-  template <int kSet>
+  // One block of results: row block i, column block j.
+  __device__ __forceinline__ f32x4 multiply(int i, int j, int32_t a_byte) const {
+    if constexpr (kMx)
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j], 0, 0, 0, b_byte[j],
+                                                              0, a_byte);
+    else
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], f32x4{0.f, 0.f, 0.f, 0.f}, 0,
+                                                              0, 0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void add(int i, int j, const f32x4& sum, float f0, float f1) {
+    if constexpr (kMx) {
+      acc[i][j] = sum;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], kGlu && j >= TN / 2 ? f1 : f0, acc[i][j][k]);
+    }
+  }
+  // Row block i's scale in stage slot kSlot: the E8M0 byte of this lane's 32 channels, or the fp32 bits.
+  __device__ __forceinline__ int32_t row_scale(uint32_t slot, int i) const {
+    const char* at = lds + slot * kScaleBytes + as_read + i * (WM * 64);
+    if constexpr (kMx) return *reinterpret_cast<const uint8_t*>(at);
+    else return *reinterpret_cast<const int32_t*>(at);
+  }
+
+  // Stage s, in slot s & 1.  Its matrix fragments are in bf, its first two row
+  // fragments in af (that of row block i is in af[i & 1]).
+  template <int kSlot>
   __device__ __forceinline__ void step(int s) {
-    lds_barrier();  // every wave is done with stage s - 1
-    const uint32_t slot = s & 1, base = slot * kStageBytes, next = (slot ^ 1) * kStageBytes;
-    const bool more = s + 1 < stages;
+    // Every wave is done with the row unit and scales of stage s - 1, and has the
+    // matrix unit of stage s in registers.
+    lds_barrier();
+    constexpr uint32_t kNext = 1 - kSlot;
+    const bool more = s + 1 < stages, more2 = s + 2 < stages;
+    const float now0 = b_scale[0], now1 = b_scale[1];
     if constexpr (!kMx) {
       if (more) {
-        b_scale[1 - kSet][0] = block_scale(bs_off, s + 1);
-        if constexpr (kGlu) b_scale[1 - kSet][1] = block_scale(bs_read, s + 1);
+        b_scale[0] = block_scale(block0, s + 1);
+        if constexpr (kGlu) b_scale[1] = block_scale(block1, s + 1);
       }
     }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      if (more) {
+    for (int i = 0; i < kTurn; ++i) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-          if (j * (kTurn / 2) / kLoads == i) load_piece(s + 1, slot ^ 1, j);
-      }
-      if (i == kTurn) {
-        wait_loads<0>();
-        lds_barrier();
-      }
-      if (i >= kTurn) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          if (kTurn + j * (TM - kTurn) / TN == i) read_matrix<1 - kSet>(next, j);
-      }
-      af[(i + 1) & 1] = i + 1 < TM ? row_fragment(base, i + 1) : row_fragment(next, 0);
-      if (i < blocks) {
-        if constexpr (kMx) {
-          const int32_t a_byte = *reinterpret_cast<const uint8_t*>(lds + base + as_read + i * (WM * 64));
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                bf[kSet][j], af[i & 1], acc[i][j], 0, 0, 0, b_byte[kSet][j], 0, a_byte);
+      for (int j = 0; j < kLoads; ++j) {
+        if (j * kTurn / kLoads != i) continue;
+        if (j < kFirstLoads) {
+          if (more) load_first(s + 1, j);
         } else {
-          const float a_scale = *reinterpret_cast<const float*>(lds + base + as_read + i * (WM * 64));
-          const float s0 = a_scale * b_scale[kSet][0];
-          const float s1 = kGlu ? a_scale * b_scale[kSet][1] : s0;
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            const f32x4 sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                bf[kSet][j], af[i & 1], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-            const float f = kGlu && j >= TN / 2 ? s1 : s0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], f, acc[i][j][k]);
-          }
+          if (more2) load_matrix(s + 2, j - kFirstLoads);
         }
+      }
+      const int32_t scale = row_scale(kSlot, i);
+      if (i > 0) af[(i + 1) & 1] = row_fragment(kSlot, i + 1);
+      if (i < blocks) {
+        const float a = __int_as_float(scale), f0 = a * now0, f1 = a * now1;
+        f32x4 sum[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sum[j] = multiply(i, j, scale);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) add(i, j, sum[j], f0, f1);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    af[1] = row_fragment(kSlot, TM - 1);
+    // Stage s + 1 has landed: only the matrix unit of s + 2 may be on its way.
+    if (more2) wait_loads<kBLoads>();
+    else wait_loads<0>();
+    lds_barrier();
+    // The last two row blocks column by column: a matrix fragment of stage s + 1
+    // takes its registers as soon as both are through.
+    const int32_t scale0 = row_scale(kSlot, kTurn), scale1 = row_scale(kSlot, kTurn + 1);
+    const float a0_ = __int_as_float(scale0), a1_ = __int_as_float(scale1);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (kTurn < blocks) {
+        const f32x4 sum0 = multiply(kTurn, j, scale0), sum1 = multiply(kTurn + 1, j, scale1);
+        add(kTurn, j, sum0, a0_ * now0, a0_ * now1);
+        add(kTurn + 1, j, sum1, a1_ * now0, a1_ * now1);
+      }
+      read_matrix(kNext, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    af[0] = row_fragment(kNext, 0);
+    af[1] = row_fragment(kNext, 1);
   }
 
   __device__ __forceinline__ void accumulate() {
@@ -219,16 +254,23 @@ struct Fp8Gemm {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) load_piece(0, 0, j);
+    for (int j = 0; j < kFirstLoads; ++j) load_first(0, j);
+#pragma unroll
+    for (int j = 0; j < kBLoads; ++j) load_matrix(0, j);
+    if (stages > 1) {
+#pragma unroll
+      for (int j = 0; j < kBLoads; ++j) load_matrix(1, j);
+    }
     if constexpr (!kMx) {
-      b_scale[0][0] = block_scale(bs_off, 0);
-      if constexpr (kGlu) b_scale[0][1] = block_scale(bs_read, 0);
+      b_scale[0] = b_scale[1] = block_scale(block0, 0);
+      if constexpr (kGlu) b_scale[1] = block_scale(block1, 0);
     }
     wait_loads<0>();
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) read_matrix<0>(0, j);
+    for (int j = 0; j < TN; ++j) read_matrix(0, j);
     af[0] = row_fragment(0, 0);
+    af[1] = row_fragment(0, 1);
     // (past the last stage, fragments are read from a slot that nobody uses)
     for (int s = 0; s < stages; s += 2) {
       step<0>(s);
@@ -247,9 +289,9 @@ struct Fp8Gemm {
 };
 
 template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, 1) void gemm_fp8_kernel(GemmArgs g) {
+__global__ __launch_bounds__(kWaves * 64, 2) void gemm_fp8_kernel(GemmArgs g) {
   typedef Fp8Gemm<kMx, kGlu, TM, TN, WM, WN> G;
-  __shared__ __align__(1024) char lds[kSlots * G::kStageBytes];
+  __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
   gemm.run();
 }
@@ -269,8 +311,8 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
 
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream) {
   const bool glu = g.act == EP_ACT_SWIGLU;
-  if (mx) return glu ? launch<true, true, 8, 8, 2, 2>(g, stream) : launch<true, false, 8, 8, 2, 2>(g, stream);
-  return glu ? launch<false, true, 8, 4, 2, 2>(g, stream) : launch<false, false, 8, 4, 2, 2>(g, stream);
+  if (mx) return glu ? launch<true, true, 8, 4, 2, 4>(g, stream) : launch<true, false, 8, 4, 2, 4>(g, stream);
+  return glu ? launch<false, true, 8, 4, 2, 4>(g, stream) : launch<false, false, 8, 4, 2, 4>(g, stream);
 }
 
 }  // namespace ep
