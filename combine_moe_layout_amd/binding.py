@@ -125,8 +125,14 @@ def _check(fn: str, status: int) -> None:
         raise EpError(fn, status, lib().ep_status_string(status).decode())
 
 
+# the current stream's handle of a device by number, without making a Stream object (2.7 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -410,55 +416,62 @@ def _width(n: int, act: int) -> int:
     return 2 * n if act == EP_ACT_SWIGLU else n
 
 
-def _operand(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, device) -> int | None:
-    """Device pointer of a contiguous tensor of this type, shape and device (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr() if t.numel() else None
+class _Call:
+    """The tensors of one call: each is checked (type, shape, device, contiguous) as its pointer is
+    taken, and outputs against every other tensor's memory."""
+    __slots__ = ("device", "ranges")
 
+    def __init__(self, first: torch.Tensor, name: str, dims: int, layout: EpLayout | None = None):
+        if first.dim() != dims:
+            raise ValueError("%s must have %d dimensions" % (name, dims))
+        if not first.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % name)
+        self.device = first.get_device()
+        self.ranges = []
+        if layout is not None and layout.expert_offsets.get_device() != self.device:
+            raise ValueError("the layout and %s are on different devices" % name)
 
-def _call(fn: str, device: torch.device, stream, *args) -> None:
-    """The entry point on `device`, with the stream as its last argument."""
-    f = getattr(lib(), fn)
-    if device.index == torch.cuda.current_device():
-        status = f(*args, _stream(stream))
-    else:
-        with torch.cuda.device(device):
+    def operand(self, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple) -> int | None:
+        """Device pointer (None stays None)."""
+        if t is None:
+            return None
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        if t.get_device() != self.device:
+            raise ValueError("%s must be a GPU tensor on the call's device %d" % (name, self.device))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        n = t.numel()
+        if n == 0:
+            return None
+        p = t.data_ptr()
+        self.ranges.append((p, p + n * dtype.itemsize, name))
+        return p
+
+    def output(self, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
+               may_be: int | None = None) -> int | None:
+        """The same for an output, which must not share memory with a tensor taken before it
+        (but may be the one at address may_be)."""
+        p = self.operand(t, name, dtype, shape)
+        if p is not None:
+            mine = self.ranges[-1]
+            for lo, hi, other in self.ranges[:-1]:
+                if lo < mine[1] and p < hi and not (lo == p == may_be):
+                    raise ValueError("%s overlaps %s" % (name, other))
+        return p
+
+    def run(self, fn: str, stream, *args) -> None:
+        """The entry point on the tensors' device, with the stream as its last argument."""
+        f = getattr(lib(), fn)
+        if self.device == torch.cuda.current_device():
             status = f(*args, _stream(stream))
-    _check(fn, status)
-
-
-def _on_gpu(t: torch.Tensor, name: str, dims: int) -> torch.device:
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions" % (name, dims))
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    return t.device
-
-
-def _layout_on(layout: EpLayout, device: torch.device) -> None:
-    if layout.expert_offsets.device != device:
-        raise ValueError("the layout is on %s, the tensors on %s" % (layout.expert_offsets.device, device))
-
-
-def _distinct(out: torch.Tensor | None, name: str, *inputs: torch.Tensor | None) -> None:
-    """An output that shares memory with an input is refused."""
-    if out is None:
-        return
-    a, n = out.data_ptr(), out.numel() * out.element_size()
-    for t in inputs:
-        if t is not None and a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < a + n:
-            raise ValueError("%s overlaps an input" % name)
+        else:
+            with torch.cuda.device(self.device):
+                status = f(*args, _stream(stream))
+        if status != EP_OK:
+            _check(fn, status)
 
 
 def ep_expert_gemm(x: torch.Tensor, weights: torch.Tensor, layout: EpLayout, out: torch.Tensor,
@@ -470,29 +483,24 @@ def ep_expert_gemm(x: torch.Tensor, weights: torch.Tensor, layout: EpLayout, out
     bf16 / fp16: all of that type.  FP8: uint8 codes, x_scales fp32 [R, K/128] ([K/128, R] with
     EP_SCALES_MN_MAJOR), weight_scales fp32 [E, W/128, K/128].  MXFP8: x_scales uint8 [R, K/32],
     weight_scales uint8 [E, W, K/32].  FP8 results are bf16.  preact [R, W]: the product itself."""
-    dev = _on_gpu(x, "x", 2)
-    _layout_on(layout, dev)
+    c = _Call(x, "x", 2, layout)
     R, E, K, N = layout.num_recv_rows, layout.num_experts, x.shape[1], out.shape[-1]
     W, base = _width(N, act), dtype & ~EP_SCALES_MN_MAJOR
-    fp8, et = base in _FP8_DTYPES, _elem(base)
-    qt = torch.uint8 if fp8 else et
-    if fp8:
-        mx = base == EP_MXFP8_E4M3
+    et = _elem(base)
+    if base in _FP8_DTYPES:
+        qt, mx = torch.uint8, base == EP_MXFP8_E4M3
         st = torch.uint8 if mx else torch.float32
         xs = (R, K // 32) if mx else (K // 128, R) if dtype & EP_SCALES_MN_MAJOR else (R, K // 128)
         ws = (E, W, K // 32) if mx else (E, W // 128, K // 128)
     else:
-        st, xs, ws = torch.float32, (), ()
+        qt, st, xs, ws = et, torch.float32, (), ()
         if x_scales is not None or weight_scales is not None:
             raise ValueError("dtype %d has no scales" % dtype)
-    _distinct(out, "out", x, weights, bias, x_scales, weight_scales, preact)
-    _distinct(preact, "preact", x, weights, bias, x_scales, weight_scales)
-    _call("ep_expert_gemm", dev, stream, _operand(x, "x", qt, (R, K), dev),
-          _operand(x_scales, "x_scales", st, xs, dev),
-          _operand(weights, "weights", qt, (E, W, K), dev),
-          _operand(weight_scales, "weight_scales", st, ws, dev),
-          _operand(bias, "bias", et, (E, W), dev), ctypes.byref(layout.struct), K, N, dtype, act,
-          _operand(preact, "preact", et, (R, W), dev), _operand(out, "out", et, (R, N), dev))
+    c.run("ep_expert_gemm", stream, c.operand(x, "x", qt, (R, K)), c.operand(x_scales, "x_scales", st, xs),
+          c.operand(weights, "weights", qt, (E, W, K)),
+          c.operand(weight_scales, "weight_scales", st, ws), c.operand(bias, "bias", et, (E, W)),
+          ctypes.byref(layout.struct), K, N, dtype, act, c.output(preact, "preact", et, (R, W)),
+          c.output(out, "out", et, (R, N)))
 
 
 def ep_expert_gemm_grad_x(dy: torch.Tensor, weights: torch.Tensor, layout: EpLayout,
@@ -500,16 +508,14 @@ def ep_expert_gemm_grad_x(dy: torch.Tensor, weights: torch.Tensor, layout: EpLay
                           preact: torch.Tensor | None = None, stream=None) -> None:
     """dy [R, N], weights [E, N, K] -> dx = (dy W_e) act'(preact): [R, K], or with EP_ACT_SWIGLU
     [R, 2K]; preact has dx's shape (none for EP_ACT_NONE)."""
-    dev = _on_gpu(dy, "dy", 2)
-    _layout_on(layout, dev)
+    c = _Call(dy, "dy", 2, layout)
     if weights.dim() != 3:
         raise ValueError("weights must have 3 dimensions")
     R, E, N, K, et = layout.num_recv_rows, layout.num_experts, dy.shape[1], weights.shape[2], _elem(dtype)
     shape = (R, _width(K, act))
-    _distinct(dx, "dx", dy, weights, preact)
-    _call("ep_expert_gemm_grad_x", dev, stream, _operand(dy, "dy", et, (R, N), dev),
-          _operand(weights, "weights", et, (E, N, K), dev), ctypes.byref(layout.struct), K, N, dtype,
-          act, _operand(preact, "preact", et, shape, dev), _operand(dx, "dx", et, shape, dev))
+    c.run("ep_expert_gemm_grad_x", stream, c.operand(dy, "dy", et, (R, N)),
+          c.operand(weights, "weights", et, (E, N, K)), ctypes.byref(layout.struct), K, N, dtype, act,
+          c.operand(preact, "preact", et, shape), c.output(dx, "dx", et, shape))
 
 
 def ep_expert_gemm_grad_w(dy: torch.Tensor, x: torch.Tensor, layout: EpLayout,
@@ -517,16 +523,13 @@ def ep_expert_gemm_grad_w(dy: torch.Tensor, x: torch.Tensor, layout: EpLayout,
                           stream=None) -> None:
     """dy [R, N], x [R, K] -> dweights [E, N, K] (and dbias [E, N]): dy_e^T x_e over the rows of
     each expert, in dtype's type or, with EP_GRAD_F32, fp32; EP_GRAD_ACCUMULATE adds."""
-    dev = _on_gpu(dy, "dy", 2)
-    _layout_on(layout, dev)
+    c = _Call(dy, "dy", 2, layout)
     R, E, N, K = layout.num_recv_rows, layout.num_experts, dy.shape[1], x.shape[-1]
     et = _elem(dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE))
     gt = torch.float32 if dtype & EP_GRAD_F32 else et
-    _distinct(dweights, "dweights", dy, x, dbias)
-    _distinct(dbias, "dbias", dy, x)
-    _call("ep_expert_gemm_grad_w", dev, stream, _operand(dy, "dy", et, (R, N), dev),
-          _operand(x, "x", et, (R, K), dev), ctypes.byref(layout.struct), K, N, dtype,
-          _operand(dweights, "dweights", gt, (E, N, K), dev), _operand(dbias, "dbias", gt, (E, N), dev))
+    c.run("ep_expert_gemm_grad_w", stream, c.operand(dy, "dy", et, (R, N)), c.operand(x, "x", et, (R, K)),
+          ctypes.byref(layout.struct), K, N, dtype, c.output(dweights, "dweights", gt, (E, N, K)),
+          c.output(dbias, "dbias", gt, (E, N)))
 
 
 def ep_linear(x: torch.Tensor, weights: torch.Tensor, out: torch.Tensor, dtype: int,
@@ -535,55 +538,48 @@ def ep_linear(x: torch.Tensor, weights: torch.Tensor, out: torch.Tensor, dtype: 
               stream=None) -> None:
     """x [rows, K], weights [W, K] -> out [rows, N] = act(x W^T + bias) + residual; W = N, or 2N
     for EP_ACT_SWIGLU.  preact [rows, W]: the product itself.  out may be the residual."""
-    dev = _on_gpu(x, "x", 2)
+    c = _Call(x, "x", 2)
     T, K, N, et = x.shape[0], x.shape[1], out.shape[-1], _elem(dtype)
     W = _width(N, act)
-    _distinct(out, "out", x, weights, bias, preact,
-              None if residual is not None and residual.data_ptr() == out.data_ptr() else residual)
-    _distinct(preact, "preact", x, weights, bias, residual)
-    _call("ep_linear", dev, stream, _operand(x, "x", et, (T, K), dev),
-          _operand(weights, "weights", et, (W, K), dev), _operand(bias, "bias", et, (W,), dev),
-          _operand(residual, "residual", et, (T, N), dev), T, K, N, dtype, act,
-          _operand(preact, "preact", et, (T, W), dev), _operand(out, "out", et, (T, N), dev))
+    res = c.operand(residual, "residual", et, (T, N))
+    c.run("ep_linear", stream, c.operand(x, "x", et, (T, K)), c.operand(weights, "weights", et, (W, K)),
+          c.operand(bias, "bias", et, (W,)), res, T, K, N, dtype, act,
+          c.output(preact, "preact", et, (T, W)), c.output(out, "out", et, (T, N), may_be=res))
 
 
 def ep_linear_grad_x(dy: torch.Tensor, weights: torch.Tensor, dx: torch.Tensor, dtype: int,
                      act: int = EP_ACT_NONE, preact: torch.Tensor | None = None, stream=None) -> None:
     """dy [rows, N], weights [N, K] -> dx = (dy W) act'(preact), as ep_expert_gemm_grad_x."""
-    dev = _on_gpu(dy, "dy", 2)
+    c = _Call(dy, "dy", 2)
     if weights.dim() != 2:
         raise ValueError("weights must have 2 dimensions")
     T, N, K, et = dy.shape[0], dy.shape[1], weights.shape[1], _elem(dtype)
     shape = (T, _width(K, act))
-    _distinct(dx, "dx", dy, weights, preact)
-    _call("ep_linear_grad_x", dev, stream, _operand(dy, "dy", et, (T, N), dev),
-          _operand(weights, "weights", et, (N, K), dev), T, K, N, dtype, act,
-          _operand(preact, "preact", et, shape, dev), _operand(dx, "dx", et, shape, dev))
+    c.run("ep_linear_grad_x", stream, c.operand(dy, "dy", et, (T, N)), c.operand(weights, "weights", et, (N, K)),
+          T, K, N, dtype, act, c.operand(preact, "preact", et, shape), c.output(dx, "dx", et, shape))
 
 
 def ep_linear_grad_w(dy: torch.Tensor, x: torch.Tensor, dweights: torch.Tensor, dtype: int,
                      dbias: torch.Tensor | None = None, stream=None) -> None:
     """dy [rows, N], x [rows, K] -> dweights [N, K] = dy^T x, dbias [N], as ep_expert_gemm_grad_w."""
-    dev = _on_gpu(dy, "dy", 2)
+    c = _Call(dy, "dy", 2)
     T, N, K = dy.shape[0], dy.shape[1], x.shape[-1]
     et = _elem(dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE))
     gt = torch.float32 if dtype & EP_GRAD_F32 else et
-    _distinct(dweights, "dweights", dy, x, dbias)
-    _distinct(dbias, "dbias", dy, x)
-    _call("ep_linear_grad_w", dev, stream, _operand(dy, "dy", et, (T, N), dev),
-          _operand(x, "x", et, (T, K), dev), T, K, N, dtype,
-          _operand(dweights, "dweights", gt, (N, K), dev), _operand(dbias, "dbias", gt, (N,), dev))
+    c.run("ep_linear_grad_w", stream, c.operand(dy, "dy", et, (T, N)), c.operand(x, "x", et, (T, K)), T, K, N,
+          dtype, c.output(dweights, "dweights", gt, (N, K)), c.output(dbias, "dbias", gt, (N,)))
 
 
 def ep_act_grad(dy: torch.Tensor, preact: torch.Tensor, dz: torch.Tensor, dtype: int, act: int,
                 stream=None) -> None:
     """dz = dy act'(preact): dy [rows, n], preact and dz [rows, n] ([rows, 2n] for EP_ACT_SWIGLU)."""
-    dev = _on_gpu(dy, "dy", 2)
+    c = _Call(dy, "dy", 2)
     T, n, et = dy.shape[0], dy.shape[1], _elem(dtype)
     shape = (T, _width(n, act))
-    _call("ep_act_grad", dev, stream, _operand(dy, "dy", et, (T, n), dev),
-          _operand(preact, "preact", et, shape, dev), T, n, dtype, act,
-          _operand(dz, "dz", et, shape, dev))
+    d, z = c.operand(dy, "dy", et, (T, n)), c.operand(preact, "preact", et, shape)
+    same = dz.data_ptr()                   # element by element: dz may be either input
+    c.run("ep_act_grad", stream, d, z, T, n, dtype, act,
+          c.output(dz, "dz", et, shape, may_be=same if act != EP_ACT_SWIGLU or same == z else None))
 
 
 def ep_combine_grad(dout: torch.Tensor, expert_out: torch.Tensor | None, topk_weights: torch.Tensor,
@@ -591,15 +587,13 @@ def ep_combine_grad(dout: torch.Tensor, expert_out: torch.Tensor | None, topk_we
                     d_topk_weights: torch.Tensor | None, dtype: int, stream=None) -> None:
     """Gradients of ep_combine (EP_BF16) or ep_combine_f16 (EP_F16): dout [T, H] -> d_expert_out
     [R, H] (used rows) and d_topk_weights fp32 [T, k] (None to skip; expert_out is then unused)."""
-    dev = _on_gpu(dout, "dout", 2)
-    _layout_on(layout, dev)
+    c = _Call(dout, "dout", 2, layout)
     T, k, R, H, et = layout.num_tokens, layout.num_topk, layout.num_recv_rows, dout.shape[1], _elem(dtype)
-    _distinct(d_expert_out, "d_expert_out", dout, expert_out, topk_weights, d_topk_weights)
-    _call("ep_combine_grad", dev, stream, _operand(dout, "dout", et, (T, H), dev),
-          _operand(expert_out, "expert_out", et, (R, H), dev),
-          _operand(topk_weights, "topk_weights", torch.float32, (T, k), dev),
-          ctypes.byref(layout.struct), H, dtype, _operand(d_expert_out, "d_expert_out", et, (R, H), dev),
-          _operand(d_topk_weights, "d_topk_weights", torch.float32, (T, k), dev))
+    c.run("ep_combine_grad", stream, c.operand(dout, "dout", et, (T, H)),
+          c.operand(expert_out, "expert_out", et, (R, H)),
+          c.operand(topk_weights, "topk_weights", torch.float32, (T, k)), ctypes.byref(layout.struct), H, dtype,
+          c.output(d_expert_out, "d_expert_out", et, (R, H)),
+          c.output(d_topk_weights, "d_topk_weights", torch.float32, (T, k)))
 
 
 def ep_dequant_fp8(q: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, stream=None) -> None:

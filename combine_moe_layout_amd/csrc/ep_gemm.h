@@ -289,7 +289,12 @@ struct TileStore {
   // lies at c ^ (r & 15): the 16 rows that one store instruction writes at the
   // same column touch every bank once.
   static constexpr int kFit = kWaveBytes / (16 * kWaveCols * 4);  // blocks of rows that fit at once
-  static constexpr int kPassBlocks = kFit >= TM ? TM : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
+  static constexpr int pass_blocks() {  // the largest part of TM that fits
+    int n = kFit < TM ? kFit : TM;
+    while (TM % n != 0) --n;
+    return n;
+  }
+  static constexpr int kPassBlocks = pass_blocks();
   static_assert(TM % kPassBlocks == 0, "whole passes");
 
   static __device__ __forceinline__ void load8(const void* p, int64_t i, float* v) {
@@ -437,6 +442,8 @@ struct TileStore {
 
 // Picks the kernel for a 16-bit product.
 hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream);
+// Forward only; rows: about how many each group has.
+hipError_t launch_gemm_few(const GemmArgs& g, int64_t rows, bool f16, hipStream_t stream);
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream);
 // launch_gemm_tile: `mode` 0 forward, 1 rows' gradient, 2 weights' gradient.
 hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, hipStream_t stream);

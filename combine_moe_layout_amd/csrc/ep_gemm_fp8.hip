@@ -14,14 +14,15 @@
 // codes themselves are off by up to 2^-4 and the result is rounded to 2^-8, and
 // it is the price of the instructions that work at twice the 16-bit rate.
 //
-// A workgroup of 8 waves makes a 256 x 256 tile, 128 x 64 to a wave (with fp32
-// scales the sums pass through vector instructions, so a wave must hold them in
-// vector registers).  A stage is 128 channels: 64 KB of codes, so two of them fit
-// LDS.  While the matrix instructions work on stage s, the row operand of stage
-// s + 1 and then the matrix operand of stage s + 2 come in (the matrix operand of
-// stage s has been in registers since stage s - 1 ended, so its slot is free).
-// Three quarters of the way stage s + 1 has landed and its matrix fragments go to
-// registers, so that it starts without waiting for LDS.
+// A workgroup of 8 waves makes a tile of 192 rows and 256 columns, 96 x 64 to a
+// wave (with fp32 scales the sums pass through vector instructions, so a wave
+// must hold them in vector registers).  A stage is 128 channels.  While the
+// matrix instructions work on stage s, both operands of stage s + 2 come in: LDS
+// holds three stages of rows (and all scales), and two of the matrix operand,
+// whose fragments of stage s have been in registers since stage s - 1 ended.
+// 192 rows are what leaves room for the third stage of rows: with 256 rows and
+// two, rows came in one stage ahead, and waiting for them made the products of
+// 65,536 rows, 256 experts take 3.25 ms.
 #include "ep_gemm.h"
 
 namespace ep {
@@ -29,7 +30,8 @@ namespace ep {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kSlots = 2;
+constexpr int kASlots = 3;  // stages of rows and of scales in LDS
+constexpr int kBSlots = 2;  // stages of the matrix operand
 constexpr int kStage = 128;  // channels, and bytes, per stage
 
 template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
@@ -37,15 +39,16 @@ struct Fp8Gemm {
   static_assert(WM * WN == kWaves, "eight waves");
   static constexpr int kRows = 16 * TM * WM, kCols = 16 * TN * WN, kWaveCols = 16 * TN;
   static constexpr int kABytes = kRows * kStage, kBBytes = kCols * kStage;
-  static constexpr int kScaleBytes = (kRows + kCols) * 4;  // one word per row of both operands
-  static constexpr int kBAt = kSlots * kABytes, kScalesAt = kBAt + kSlots * kBBytes;
-  static constexpr int kLdsBytes = kScalesAt + kSlots * kScaleBytes;
+  static constexpr int kScaleBytes = (256 + kCols) * 4;  // one word per row of both operands
+  static constexpr int kBAt = kASlots * kABytes, kScalesAt = kBAt + kBSlots * kBBytes;
+  static constexpr int kLdsBytes = kScalesAt + kASlots * kScaleBytes;
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
   static_assert(kBLoads == 4 && kWaveCols % 64 == 0, "a wave loads half of a wave's columns");
-  static_assert(kRows == 256 && kCols == 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
-  static constexpr int kWaveBytes = kScalesAt / kWaves;
+  static_assert(kRows <= 256 && kRows % 64 == 0 && kCols == 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
+  static constexpr int kWaveBytes = kScalesAt / kWaves / 1024 * 1024;
   typedef TileStore<kForward, false, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
+  static constexpr int kRing = 4;  // row fragments in registers: two in use, two read ahead
   static constexpr int kTurn = TM - 2;  // the row of blocks before which stage s + 1 has landed
 
   const GemmArgs& g;
@@ -58,9 +61,10 @@ struct Fp8Gemm {
   uint32_t a_off[kALoads], b_off[2], s_off;
   uint32_t a_read, b_read, as_read, bs_read;
   uint32_t block0, block1;  // fp32 scales: index of the wave's first block, of its ups'
-  int wm, wn, lane, wave;
+  int wm, wn, lane, wave, turn;
   f32x4 acc[TM][TN];
-  i32x8 af[2], bf[TN];
+  i32x8 af[kRing], bf[TN];
+  int32_t scale[TM];  // the row blocks' scales: an E8M0 byte, or the bits of an fp32
   float b_scale[2];  // fp32 scales of the wave's columns: gates (or all), ups
   int32_t b_byte[kMx ? TN : 1];
 
@@ -83,6 +87,7 @@ struct Fp8Gemm {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
     wn = wave % WN;
+    turn = wave / 4;
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
     stages = g.reduce / kStage;
     blocks = __builtin_amdgcn_readfirstlane(((t.rows + 15) / 16 - wm + WM - 1) / WM);
@@ -118,26 +123,28 @@ struct Fp8Gemm {
       s_off = (uint32_t)(min(p, t.rows - 1) * g.a_scale_row * 4);
     }
     as_read = kScalesAt + (wm * 16 + m) * 4 + (kMx ? q : 0);
-    bs_read = kScalesAt + kRows * 4 + (wn * kWaveCols + m) * 4 + q;
+    bs_read = kScalesAt + 256 * 4 + (wn * kWaveCols + m) * 4 + q;
     // The wave's columns (32 gates and 32 ups, or 64) lie in one block of 128 each.
     const int64_t per_row = g.ldb / 128;
     block0 = (uint32_t)(matrix_row(wn * kWaveCols) / 128 * per_row);
     block1 = (uint32_t)(matrix_row(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
   }
 
-  // Loads of the row operand and of the scales of stage s, and of the matrix operand.
-  static constexpr int kFirstLoads = kALoads + 1, kLoads = kFirstLoads + kBLoads;
-  __device__ __forceinline__ void load_first(int s, int j) const {
-    const uint32_t slot = s & 1;
-    if (j < kALoads)
+  // Load j of stage s: of the row operand (into slot `slot`), of the scales, of
+  // the matrix operand.
+  static constexpr int kLoads = kALoads + 1 + kBLoads;
+  __device__ __forceinline__ void load_piece(int s, uint32_t slot, int j) const {
+    if (j < kALoads) {
       load16_to_lds(a0 + s * kStage, a_off[j < kALoads ? j : 0],
                     lds0 + slot * kABytes + (wave * kALoads + j) * 1024);
-    else
+    } else if (j == kALoads) {
       load4_to_lds(s0 + s * s_step, s_off,
                    lds0 + kScalesAt + slot * kScaleBytes + (kMx ? wave : wave & 3) * 256);
-  }
-  __device__ __forceinline__ void load_matrix(int s, int j) const {
-    load16_to_lds(b0 + s * kStage + (int64_t)j * 8 * g.ldb, b_off[j & 1], lds0 + kBAt + (s & 1) * kBBytes + (wave * kBLoads + j) * 1024);
+    } else {
+      const int i = j - kALoads - 1;
+      load16_to_lds(b0 + s * kStage + (int64_t)i * 8 * g.ldb, b_off[i & 1],
+                    lds0 + kBAt + (s & 1) * kBBytes + (wave * kBLoads + i) * 1024);
+    }
   }
 
   // Lane 16 q + m holds channels 16 q .. 16 q + 15 and 64 + 16 q .. of row m
@@ -151,8 +158,8 @@ struct Fp8Gemm {
   __device__ __forceinline__ i32x8 row_fragment(uint32_t slot, int i) const {
     return read_fragment(slot * kABytes + a_read + i * (WM * 16 * kStage));
   }
-  __device__ __forceinline__ void read_matrix(uint32_t slot, int j) {
-    bf[j] = read_fragment(slot * kBBytes + b_read + j * (16 * kStage));
+  __device__ __forceinline__ void read_matrix(uint32_t b_slot, uint32_t slot, int j) {
+    bf[j] = read_fragment(b_slot * kBBytes + b_read + j * (16 * kStage));
     if constexpr (kMx)
       b_byte[j] = *reinterpret_cast<const uint8_t*>(lds + slot * kScaleBytes + bs_read + j * 64);
   }
@@ -163,39 +170,40 @@ struct Fp8Gemm {
   }
 
   // One block of results: row block i, column block j.
-  __device__ __forceinline__ f32x4 multiply(int i, int j, int32_t a_byte) const {
+  __device__ __forceinline__ f32x4 multiply(int i, int j) const {
     if constexpr (kMx)
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j], 0, 0, 0, b_byte[j],
-                                                              0, a_byte);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i % kRing], acc[i][j], 0, 0, 0,
+                                                              b_byte[j], 0, scale[i]);
     else
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], f32x4{0.f, 0.f, 0.f, 0.f}, 0,
-                                                              0, 0, 0, 0, 0);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i % kRing], f32x4{0.f, 0.f, 0.f, 0.f},
+                                                              0, 0, 0, 0, 0, 0);
   }
-  __device__ __forceinline__ void add(int i, int j, const f32x4& sum, float f0, float f1) {
+  __device__ __forceinline__ void add(int i, int j, const f32x4& sum, const float* b) {
     if constexpr (kMx) {
       acc[i][j] = sum;
     } else {
+      const float f = __int_as_float(scale[i]) * b[kGlu && j >= TN / 2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], kGlu && j >= TN / 2 ? f1 : f0, acc[i][j][k]);
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], f, acc[i][j][k]);
     }
   }
-  // Row block i's scale in stage slot kSlot: the E8M0 byte of this lane's 32 channels, or the fp32 bits.
+  // Row block i's scale in slot `slot`: the E8M0 byte of this lane's 32 channels, or the fp32 bits.
   __device__ __forceinline__ int32_t row_scale(uint32_t slot, int i) const {
     const char* at = lds + slot * kScaleBytes + as_read + i * (WM * 64);
     if constexpr (kMx) return *reinterpret_cast<const uint8_t*>(at);
     else return *reinterpret_cast<const int32_t*>(at);
   }
 
-  // Stage s, in slot s & 1.  Its matrix fragments are in bf, its first two row
-  // fragments in af (that of row block i is in af[i & 1]).
-  template <int kSlot>
-  __device__ __forceinline__ void step(int s) {
-    // Every wave is done with the row unit and scales of stage s - 1, and has the
-    // matrix unit of stage s in registers.
-    lds_barrier();
-    constexpr uint32_t kNext = 1 - kSlot;
+  // Stage s, its rows in slot `now`, those of the next two stages in `next` and
+  // `after`.  Its matrix fragments are in bf, its scales in `scale`, its first two
+  // row fragments in af.
+  __device__ __forceinline__ void step(int s, uint32_t now, uint32_t next, uint32_t after) {
+    // Every wave is done with the rows and scales of stage s - 1, and has the
+    // matrix operand of stage s in registers (the youngest reads are of this
+    // stage's rows and scales).
+    lds_barrier<kYoung>();
     const bool more = s + 1 < stages, more2 = s + 2 < stages;
-    const float now0 = b_scale[0], now1 = b_scale[1];
+    const float b_now[2] = {b_scale[0], b_scale[1]};
     if constexpr (!kMx) {
       if (more) {
         b_scale[0] = block_scale(block0, s + 1);
@@ -204,48 +212,60 @@ struct Fp8Gemm {
     }
 #pragma unroll
     for (int i = 0; i < kTurn; ++i) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        if (j * kTurn / kLoads != i) continue;
-        if (j < kFirstLoads) {
-          if (more) load_first(s + 1, j);
-        } else {
-          if (more2) load_matrix(s + 2, j - kFirstLoads);
-        }
-      }
-      const int32_t scale = row_scale(kSlot, i);
-      if (i > 0) af[(i + 1) & 1] = row_fragment(kSlot, i + 1);
+      load_in_row(i, more2, s, after);
+      af[(i + 2) % kRing] = row_fragment(now, i + 2);
       if (i < blocks) {
-        const float a = __int_as_float(scale), f0 = a * now0, f1 = a * now1;
         f32x4 sum[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sum[j] = multiply(i, j, scale);
+        for (int j = 0; j < TN; ++j) sum[j] = multiply(i, j);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) add(i, j, sum[j], f0, f1);
+        for (int j = 0; j < TN; ++j) add(i, j, sum[j], b_now);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    af[1] = row_fragment(kSlot, TM - 1);
-    // Stage s + 1 has landed: only the matrix unit of s + 2 may be on its way.
-    if (more2) wait_loads<kBLoads>();
-    else wait_loads<0>();
-    lds_barrier();
+    // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
+    if (!more2) wait_loads<0>();
+    else if (turn == 0) wait_loads<kLoads>();
+    else wait_loads<issued_late(kTurn)>();
+    lds_barrier<15>();
     // The last two row blocks column by column: a matrix fragment of stage s + 1
     // takes its registers as soon as both are through.
-    const int32_t scale0 = row_scale(kSlot, kTurn), scale1 = row_scale(kSlot, kTurn + 1);
-    const float a0_ = __int_as_float(scale0), a1_ = __int_as_float(scale1);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if (kTurn < blocks) {
-        const f32x4 sum0 = multiply(kTurn, j, scale0), sum1 = multiply(kTurn + 1, j, scale1);
-        add(kTurn, j, sum0, a0_ * now0, a0_ * now1);
-        add(kTurn + 1, j, sum1, a1_ * now0, a1_ * now1);
+        const f32x4 sum0 = multiply(kTurn, j), sum1 = multiply(kTurn + 1, j);
+        add(kTurn, j, sum0, b_now);
+        add(kTurn + 1, j, sum1, b_now);
       }
-      read_matrix(kNext, j);
+      if (j % 2 == 0) load_in_row(kTurn + j / 2, more2, s, after);
+      read_matrix((s + 1) & 1, next, j);
       __builtin_amdgcn_sched_barrier(0);
     }
-    af[0] = row_fragment(kNext, 0);
-    af[1] = row_fragment(kNext, 1);
+    read_rows(next);
+  }
+  // Each SIMD has one of the first four waves and one of the others; the former
+  // load in the first half of the rows, the latter in the second.  A load holds
+  // its wave until the address unit has taken it (16 cycles each, one unit for
+  // all waves), and only the other wave keeps the matrix unit busy then.
+  static constexpr int kHalf = TM / 2, kPieces = (kLoads + kHalf - 1) / kHalf;
+  static constexpr int issued_late(int row) {
+    const int n = (row - kHalf) * kPieces;
+    return n < kLoads ? n : kLoads;
+  }
+  static_assert(TN == 4 && TM % 2 == 0, "the last two rows go in four columns");
+  __device__ __forceinline__ void load_in_row(int i, bool more2, int s, uint32_t slot) const {
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+      const int j = i % kHalf * kPieces + n;
+      if (more2 && turn == i / kHalf && j < kLoads) load_piece(s + 2, slot, j);
+    }
+  }
+  static constexpr int kYoung = 4 + TM;
+  __device__ __forceinline__ void read_rows(uint32_t slot) {
+    af[0] = row_fragment(slot, 0);
+    af[1] = row_fragment(slot, 1);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) scale[i] = row_scale(slot, i);
   }
 
   __device__ __forceinline__ void accumulate() {
@@ -254,27 +274,29 @@ struct Fp8Gemm {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kFirstLoads; ++j) load_first(0, j);
-#pragma unroll
-    for (int j = 0; j < kBLoads; ++j) load_matrix(0, j);
+    for (int j = 0; j < kLoads; ++j) load_piece(0, 0, j);
     if (stages > 1) {
 #pragma unroll
-      for (int j = 0; j < kBLoads; ++j) load_matrix(1, j);
+      for (int j = 0; j < kLoads; ++j) load_piece(1, 1, j);
     }
     if constexpr (!kMx) {
       b_scale[0] = b_scale[1] = block_scale(block0, 0);
       if constexpr (kGlu) b_scale[1] = block_scale(block1, 0);
     }
-    wait_loads<0>();
+    if (stages > 1) wait_loads<kLoads>();
+    else wait_loads<0>();
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) read_matrix(0, j);
-    af[0] = row_fragment(0, 0);
-    af[1] = row_fragment(0, 1);
+    for (int j = 0; j < TN; ++j) read_matrix(0, 0, j);
+    read_rows(0);
     // (past the last stage, fragments are read from a slot that nobody uses)
-    for (int s = 0; s < stages; s += 2) {
-      step<0>(s);
-      if (s + 1 < stages) step<1>(s + 1);
+    uint32_t now = 0, next = 1, after = 2;
+    for (int s = 0; s < stages; ++s) {
+      step(s, now, next, after);
+      const uint32_t free = now;
+      now = next;
+      next = after;
+      after = free;
     }
   }
 
@@ -311,8 +333,8 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
 
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream) {
   const bool glu = g.act == EP_ACT_SWIGLU;
-  if (mx) return glu ? launch<true, true, 8, 4, 2, 4>(g, stream) : launch<true, false, 8, 4, 2, 4>(g, stream);
-  return glu ? launch<false, true, 8, 4, 2, 4>(g, stream) : launch<false, false, 8, 4, 2, 4>(g, stream);
+  if (mx) return glu ? launch<true, true, 6, 4, 2, 4>(g, stream) : launch<true, false, 6, 4, 2, 4>(g, stream);
+  return glu ? launch<false, true, 6, 4, 2, 4>(g, stream) : launch<false, false, 6, 4, 2, 4>(g, stream);
 }
 
 }  // namespace ep

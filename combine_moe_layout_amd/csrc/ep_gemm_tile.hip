@@ -486,11 +486,24 @@ hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, h
   return f16 ? launch_mode<true>(g, mode, large, stream) : launch_mode<false>(g, mode, large, stream);
 }
 
-// 256 x 256 tiles where the groups have the rows for them and there are enough
-// tiles for every CU; 128 x 128 otherwise.
+// Which kernel.  Few rows: tiles of 128 x 128 stream the matrix at 6.1 TB/s if
+// there are enough of them, but one tile takes 0.55 us for every 64 of the
+// reduction, however few there are; the kernel for few rows fills the GPU from
+// 4096 columns on, and reads a once for every 16 columns.  Measured with a
+// reduction of 7168, few against tiles: 16 rows, 4096 columns (32 tiles) 19
+// against 89 us, 16,384 columns (128 tiles) 53 against 62; 64 experts of 16 rows
+// and 2048 columns (1024 tiles) 617 against 313; 64 rows, 16,384 columns 167
+// against 65.  Hence its limit of 128 tiles, fewer for more rows.
+// Otherwise 256 x 256 tiles where the groups have the rows for them and there
+// are enough tiles for every CU.
 hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream) {
-  const int64_t rows = mode == kWeightsGrad ? g.out_rows : g.groups.wanted / g.groups.E;
-  const int64_t tiles = (int64_t)g.groups.E * ((rows + 255) / 256) * ((g.out_cols + 255) / 256);
+  const RowGroups& r = g.groups;
+  const int64_t rows = mode == kWeightsGrad ? g.out_rows : (r.wanted + r.E - 1) / r.E;
+  const int64_t groups = mode == kWeightsGrad || r.wanted > r.E ? r.E : r.wanted;
+  const int64_t columns = (int64_t)g.out_cols * (mode == kForward && g.act == EP_ACT_SWIGLU ? 2 : 1);
+  if (mode == kForward && rows <= 64 && groups * ((columns + 127) / 128) * ((rows + 15) / 16) <= 128)
+    return launch_gemm_few(g, rows, f16, stream);
+  const int64_t tiles = groups * ((rows + 255) / 256) * ((columns + 255) / 256);
   return launch_gemm_tile(g, mode, f16, rows >= 192 && tiles >= kChipCUs, stream);
 }
 
