@@ -5,11 +5,12 @@
 //   dy[slot[t,j]] = w[t,j] dout[t]          (rounded once)
 //   dw[t,j]       = sum_h dout[t,h] y[slot[t,j],h]   (fp32; 0 for a pair without a row)
 // Bound by HBM: dout is read once, every used row of y read once and of dy
-// written once.  One workgroup holds a token's dout row in registers, 16 bytes
-// to a lane, and walks its pairs, all of whose y rows are loaded before the
-// first is used; the dot products meet in LDS in a fixed order, so the result
-// does not depend on timing.  Small batches split a token's pairs over
-// workgroups (each reads dout, from L2) so that every CU has work.
+// written once.  A workgroup holds a token's dout row in registers, 16 bytes
+// to a lane, and takes up to four of its pairs, all of whose y rows are loaded
+// before the first is used (dout comes from L2 for the others); the dot products
+// meet in LDS in a fixed order, so the result does not depend on timing.
+#include <type_traits>
+
 #include "ep_gemm.h"
 
 namespace ep {
@@ -17,7 +18,7 @@ namespace ep {
 namespace {
 
 constexpr int kMaxLanes = 1024;
-constexpr int kPairsAtOnce = 8;
+constexpr int kMostPairs = 4;
 
 template <bool kF16>
 __device__ __forceinline__ void unpack8(const u32x4& d, float* f) {
@@ -34,45 +35,63 @@ __device__ __forceinline__ u32x4 pack8_rne(const float* f) {
                elem_rne2<kF16>(f[6], f[7])};
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sums of N values (a power of two) over the 64 lanes of a wave.  In the first
+// log2(N) steps the two lanes of a pair hand each other half of their values, so
+// N - 1 exchanges leave one value to a lane, and the other steps take one each (7
+// exchanges for 4 values instead of 24).  Returns the sum of value `index`.
+template <int N>
+__device__ __forceinline__ float wave_sums(float (&v)[N], int& index) {
+  const int lane = threadIdx.x & 63;
+  index = 0;
+  int mask = 1;
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  for (int n = N / 2; n >= 1; n /= 2, mask *= 2) {
+    const bool high = lane & mask;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = high ? v[n + i] : v[i], give = high ? v[i] : v[n + i];
+      v[i] = keep + __shfl_xor(give, mask, 64);
+    }
+    index += high ? n : 0;
+  }
+  float s = v[0];
+  for (; mask < 64; mask *= 2) s += __shfl_xor(s, mask, 64);
+  return s;
 }
 
 // lanes: threads of one token (a multiple of 64); the block holds blockDim / lanes
-// tokens.  pairs: pairs of one workgroup (at most kPairsAtOnce), splits: workgroups per token.
-template <bool kF16, bool kDw>
+// tokens.  kPairs: pairs of one workgroup, splits: workgroups per token.
+template <bool kF16, bool kDw, int kPairs>
 __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
     const u32x4* __restrict__ dout, const u32x4* __restrict__ y, const float* __restrict__ w,
     const int32_t* __restrict__ slot, int64_t tokens, int32_t k, int32_t vecs, int32_t lanes,
-    int32_t pairs, int32_t splits, u32x4* __restrict__ dy, float* __restrict__ dw) {
-  __shared__ float part[kMaxLanes / 64][kPairsAtOnce];
+    int32_t splits, u32x4* __restrict__ dy, float* __restrict__ dw) {
+  __shared__ float part[kMaxLanes / 64][kPairs];
   const int local = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int64_t block = blockIdx.x;
   const int64_t t = block / splits * (blockDim.x / lanes) + local;
-  const int j0 = (int)(block % splits) * pairs;
-  const int n = t < tokens ? min(pairs, k - j0) : 0;
-  int64_t row[kPairsAtOnce];
-  float weight[kPairsAtOnce], dot[kPairsAtOnce];
+  const int j0 = (int)(block % splits) * kPairs;
+  const int n = t < tokens ? min(kPairs, k - j0) : 0;
+  int64_t row[kPairs];
+  float weight[kPairs], dot[kPairs];
 #pragma unroll
-  for (int j = 0; j < kPairsAtOnce; ++j) {
+  for (int j = 0; j < kPairs; ++j) {
     row[j] = j < n ? (int64_t)slot[t * k + j0 + j] : -1;
     weight[j] = j < n ? w[t * k + j0 + j] : 0.f;
     dot[j] = 0.f;
   }
   if (n > 0) {
     for (int v = lane; v < vecs; v += lanes) {
-      u32x4 rows[kPairsAtOnce];
+      u32x4 rows[kPairs];
       if constexpr (kDw) {
 #pragma unroll
-        for (int j = 0; j < kPairsAtOnce; ++j)
+        for (int j = 0; j < kPairs; ++j)
           if (row[j] >= 0) rows[j] = load_nt(y + row[j] * vecs + v);
       }
       float d[8];
       unpack8<kF16>(dout[t * vecs + v], d);
 #pragma unroll
-      for (int j = 0; j < kPairsAtOnce; ++j) {
+      for (int j = 0; j < kPairs; ++j) {
         if (row[j] < 0) continue;
         if constexpr (kDw) {
           float f[8];
@@ -89,11 +108,13 @@ __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
   }
   if constexpr (kDw) {
     const int wave = threadIdx.x >> 6, waves = lanes >> 6;
+    constexpr int kSums = kPairs == 3 ? 4 : kPairs;
+    float sums[kSums] = {};
 #pragma unroll
-    for (int j = 0; j < kPairsAtOnce; ++j) {
-      const float s = wave_sum(dot[j]);
-      if ((threadIdx.x & 63) == 0) part[wave][j] = s;
-    }
+    for (int j = 0; j < kPairs; ++j) sums[j] = dot[j];
+    int index;
+    const float total = wave_sums<kSums>(sums, index);
+    if ((threadIdx.x & 63) < kSums && index < kPairs) part[wave][index] = total;
     __syncthreads();
     if (lane < n) {
       float s = 0.f;
@@ -141,19 +162,33 @@ hipError_t combine_grad(const void* dout, const void* y, const float* w, const e
   if (lanes > kMaxLanes) lanes = kMaxLanes;
   const int32_t tokens_per_block = lanes >= 256 ? 1 : 256 / lanes;
   const int64_t token_blocks = (L.num_tokens + tokens_per_block - 1) / tokens_per_block;
-  // At least four workgroups to a CU while there are pairs to split.
-  int32_t pairs = L.num_topk < kPairsAtOnce ? L.num_topk : kPairsAtOnce;
-  while (pairs > 1 && token_blocks * ((L.num_topk + pairs - 1) / pairs) < 4 * kChipCUs) pairs = (pairs + 1) / 2;
+  // At most four pairs to a workgroup, shared out evenly; one for the smallest
+  // batches.  Measured at hidden 7168, top-8: 128 tokens 13.1 us with one pair,
+  // 10.6 with two, 9.5 with four; 512 tokens 29 us with up to four, 36 with eight;
+  // 8192 tokens 384 us with four, 389 with two, 387 with eight; 8 tokens 4.4 us
+  // with one, 5.3 with four.
+  int32_t pairs = 1;
+  if (token_blocks >= 64) {
+    const int32_t parts = (L.num_topk + kMostPairs - 1) / kMostPairs;
+    pairs = (L.num_topk + parts - 1) / parts;
+  }
   const int32_t splits = (L.num_topk + pairs - 1) / pairs;
   const int64_t blocks = token_blocks * splits;
   if (!grid_fits(blocks, lanes * tokens_per_block)) return hipErrorInvalidValue;
   const auto args = [&](auto kernel) {
     kernel<<<(uint32_t)blocks, lanes * tokens_per_block, 0, stream>>>(
         static_cast<const u32x4*>(dout), static_cast<const u32x4*>(y), w, L.slot_idx, L.num_tokens,
-        L.num_topk, vecs, lanes, pairs, splits, static_cast<u32x4*>(dy), dw);
+        L.num_topk, vecs, lanes, splits, static_cast<u32x4*>(dy), dw);
   };
-  if (dw != nullptr) args(combine_grad_kernel<kF16, true>);
-  else args(combine_grad_kernel<kF16, false>);
+  const auto sized = [&](auto with_dw) {
+    constexpr bool kDw = decltype(with_dw)::value;
+    if (pairs == 4) args(combine_grad_kernel<kF16, kDw, 4>);
+    else if (pairs == 3) args(combine_grad_kernel<kF16, kDw, 3>);
+    else if (pairs == 2) args(combine_grad_kernel<kF16, kDw, 2>);
+    else args(combine_grad_kernel<kF16, kDw, 1>);
+  };
+  if (dw != nullptr) sized(std::true_type());
+  else sized(std::false_type());
   return hipGetLastError();
 }
 
