@@ -39,24 +39,26 @@ __device__ __forceinline__ u32x4 pack8_rne(const float* f) {
 // log2(N) steps the two lanes of a pair hand each other half of their values, so
 // N - 1 exchanges leave one value to a lane, and the other steps take one each (7
 // exchanges for 4 values instead of 24).  Returns the sum of value `index`.
-template <int N>
-__device__ __forceinline__ float wave_sums(float (&v)[N], int& index) {
-  const int lane = threadIdx.x & 63;
-  index = 0;
-  int mask = 1;
+template <int N, int kMask = 1>
+__device__ __forceinline__ float wave_sums(const float (&v)[N], int& index) {
+  if constexpr (N == 1) {
+    index = 0;
+    float s = v[0];
 #pragma unroll
-  for (int n = N / 2; n >= 1; n /= 2, mask *= 2) {
-    const bool high = lane & mask;
+    for (int mask = kMask; mask < 64; mask *= 2) s += __shfl_xor(s, mask, 64);
+    return s;
+  } else {
+    const bool high = threadIdx.x & kMask;
+    float half[N / 2];
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float keep = high ? v[n + i] : v[i], give = high ? v[i] : v[n + i];
-      v[i] = keep + __shfl_xor(give, mask, 64);
+    for (int i = 0; i < N / 2; ++i) {
+      const float keep = high ? v[N / 2 + i] : v[i], give = high ? v[i] : v[N / 2 + i];
+      half[i] = keep + __shfl_xor(give, kMask, 64);
     }
-    index += high ? n : 0;
+    const float s = wave_sums<N / 2, kMask * 2>(half, index);
+    index += high ? N / 2 : 0;
+    return s;
   }
-  float s = v[0];
-  for (; mask < 64; mask *= 2) s += __shfl_xor(s, mask, 64);
-  return s;
 }
 
 // lanes: threads of one token (a multiple of 64); the block holds blockDim / lanes
@@ -72,37 +74,44 @@ __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
   const int64_t t = block / splits * (blockDim.x / lanes) + local;
   const int j0 = (int)(block % splits) * kPairs;
   const int n = t < tokens ? min(kPairs, k - j0) : 0;
-  int64_t row[kPairs];
-  float weight[kPairs], dot[kPairs];
-#pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
-    row[j] = j < n ? (int64_t)slot[t * k + j0 + j] : -1;
-    weight[j] = j < n ? w[t * k + j0 + j] : 0.f;
-    dot[j] = 0.f;
-  }
+  float dot[kPairs] = {};
   if (n > 0) {
-    for (int v = lane; v < vecs; v += lanes) {
-      u32x4 rows[kPairs];
-      if constexpr (kDw) {
+    // All slots and weights at once: a pair past the last reads the last one's.
+    int64_t row[kPairs];
+    float weight[kPairs];
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j)
-          if (row[j] >= 0) rows[j] = load_nt(y + row[j] * vecs + v);
+    for (int j = 0; j < kPairs; ++j) {
+      const int64_t p = t * k + j0 + min(j, n - 1);
+      row[j] = slot[p];
+      weight[j] = w[p];
+    }
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+      if (j >= n) row[j] = -1;
+    for (int v = lane; v < vecs; v += lanes) {
+      const u32x4 mine = dout[t * vecs + v];
+      u32x4 rows[kPairs];
+      if constexpr (kDw) {  // a pair without a row reads row 0, and its sum is dropped
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) rows[j] = load_nt(y + max(row[j], (int64_t)0) * vecs + v);
       }
       float d[8];
-      unpack8<kF16>(dout[t * vecs + v], d);
+      unpack8<kF16>(mine, d);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        if (row[j] < 0) continue;
         if constexpr (kDw) {
-          float f[8];
+          float f[8], sum = dot[j];
           unpack8<kF16>(rows[j], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+          for (int i = 0; i < 8; ++i) sum = fmaf(d[i], f[i], sum);
+          dot[j] = row[j] >= 0 ? sum : 0.f;
         }
-        float o[8];
+        if (row[j] >= 0) {
+          float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = weight[j] * d[i];
-        store_nt(dy + row[j] * vecs + v, pack8_rne<kF16>(o));
+          for (int i = 0; i < 8; ++i) o[i] = weight[j] * d[i];
+          store_nt(dy + row[j] * vecs + v, pack8_rne<kF16>(o));
+        }
       }
     }
   }
