@@ -49,6 +49,7 @@ struct Fp8Gemm {
   typedef TileStore<kForward, false, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
   static constexpr int kRing = 4;  // row fragments in registers: two in use, two read ahead
+  static_assert(TM % kRing == 2, "two stages leave the ring where it was");
   static constexpr int kTurn = TM - 2;  // the row of blocks before which stage s + 1 has landed
 
   const GemmArgs& g;
@@ -63,10 +64,10 @@ struct Fp8Gemm {
   uint32_t block0, block1;  // fp32 scales: index of the wave's first block, of its ups'
   int wm, wn, lane, wave, turn;
   f32x4 acc[TM][TN];
-  i32x8 af[kRing], bf[TN];
-  int32_t scale[TM];  // the row blocks' scales: an E8M0 byte, or the bits of an fp32
+  i32x8 af[kRing], bf[2][TN];
+  int32_t scale[2][TM];  // the row blocks' scales: an E8M0 byte, or the bits of an fp32
   float b_scale[2];  // fp32 scales of the wave's columns: gates (or all), ups
-  int32_t b_byte[kMx ? TN : 1];
+  int32_t b_byte[2][kMx ? TN : 1];
 
   __device__ __forceinline__ Fp8Gemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
@@ -158,10 +159,11 @@ struct Fp8Gemm {
   __device__ __forceinline__ i32x8 row_fragment(uint32_t slot, int i) const {
     return read_fragment(slot * kABytes + a_read + i * (WM * 16 * kStage));
   }
+  template <int kSet>
   __device__ __forceinline__ void read_matrix(uint32_t b_slot, uint32_t slot, int j) {
-    bf[j] = read_fragment(b_slot * kBBytes + b_read + j * (16 * kStage));
+    bf[kSet][j] = read_fragment(b_slot * kBBytes + b_read + j * (16 * kStage));
     if constexpr (kMx)
-      b_byte[j] = *reinterpret_cast<const uint8_t*>(lds + slot * kScaleBytes + bs_read + j * 64);
+      b_byte[kSet][j] = *reinterpret_cast<const uint8_t*>(lds + slot * kScaleBytes + bs_read + j * 64);
   }
   // A block's fp32 scale, by a scalar load (it must not wait for the loads to LDS).
   __device__ __forceinline__ float block_scale(uint32_t index, int s) const {
@@ -169,20 +171,24 @@ struct Fp8Gemm {
     return ((cfloat*)(uintptr_t)bs0)[__builtin_amdgcn_readfirstlane(index) + s];
   }
 
-  // One block of results: row block i, column block j.
+  // One block of results: row block i, column block j.  Row block i's fragment is
+  // in af[(2 kSet + i) % kRing].
+  template <int kSet>
   __device__ __forceinline__ f32x4 multiply(int i, int j) const {
+    const i32x8& a = af[(2 * kSet + i) % kRing];
     if constexpr (kMx)
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i % kRing], acc[i][j], 0, 0, 0,
-                                                              b_byte[j], 0, scale[i]);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[kSet][j], a, acc[i][j], 0, 0, 0, b_byte[kSet][j],
+                                                              0, scale[kSet][i]);
     else
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i % kRing], f32x4{0.f, 0.f, 0.f, 0.f},
-                                                              0, 0, 0, 0, 0, 0);
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[kSet][j], a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
+                                                              0, 0, 0);
   }
+  template <int kSet>
   __device__ __forceinline__ void add(int i, int j, const f32x4& sum, const float* b) {
     if constexpr (kMx) {
       acc[i][j] = sum;
     } else {
-      const float f = __int_as_float(scale[i]) * b[kGlu && j >= TN / 2];
+      const float f = __int_as_float(scale[kSet][i]) * b[kGlu && j >= TN / 2];
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], f, acc[i][j][k]);
     }
@@ -194,14 +200,16 @@ struct Fp8Gemm {
     else return *reinterpret_cast<const int32_t*>(at);
   }
 
-  // Stage s, its rows in slot `now`, those of the next two stages in `next` and
-  // `after`.  Its matrix fragments are in bf, its scales in `scale`, its first two
-  // row fragments in af.
+  // Stage s, kSet = s & 1, its rows in slot `now`, those of the next two stages in
+  // `next` and `after`.  Its matrix fragments and scales are in the registers of
+  // kSet, its first two row fragments in af; the next stage's are read as soon as
+  // it has landed, in the last two row blocks.
+  template <int kSet>
   __device__ __forceinline__ void step(int s, uint32_t now, uint32_t next, uint32_t after) {
     // Every wave is done with the rows and scales of stage s - 1, and has the
-    // matrix operand of stage s in registers (the youngest reads are of this
-    // stage's rows and scales).
-    lds_barrier<kYoung>();
+    // matrix operand of stage s in registers (the youngest two reads are of this
+    // stage's second row fragment).
+    lds_barrier<2>();
     const bool more = s + 1 < stages, more2 = s + 2 < stages;
     const float b_now[2] = {b_scale[0], b_scale[1]};
     if constexpr (!kMx) {
@@ -211,37 +219,36 @@ struct Fp8Gemm {
       }
     }
 #pragma unroll
-    for (int i = 0; i < kTurn; ++i) {
+    for (int i = 0; i < TM; ++i) {
+      if (i == kTurn) {
+        // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
+        if (!more2) wait_loads<0>();
+        else if (turn == 0) wait_loads<kLoads>();
+        else wait_loads<issued_late(kTurn)>();
+        lds_barrier<15>();
+        read_scales<1 - kSet>(next);
+      }
       load_in_row(i, more2, s, after);
-      af[(i + 2) % kRing] = row_fragment(now, i + 2);
+      const int f = i + 2;
+      af[(2 * kSet + f) % kRing] = f < TM ? row_fragment(now, f) : row_fragment(next, f - TM);
+      if (i == kTurn) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) read_matrix<1 - kSet>((s + 1) & 1, next, j);
+      }
       if (i < blocks) {
         f32x4 sum[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sum[j] = multiply(i, j);
+        for (int j = 0; j < TN; ++j) sum[j] = multiply<kSet>(i, j);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) add(i, j, sum[j], b_now);
+        for (int j = 0; j < TN; ++j) add<kSet>(i, j, sum[j], b_now);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
-    if (!more2) wait_loads<0>();
-    else if (turn == 0) wait_loads<kLoads>();
-    else wait_loads<issued_late(kTurn)>();
-    lds_barrier<15>();
-    // The last two row blocks column by column: a matrix fragment of stage s + 1
-    // takes its registers as soon as both are through.
+  }
+  template <int kSet>
+  __device__ __forceinline__ void read_scales(uint32_t slot) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if (kTurn < blocks) {
-        const f32x4 sum0 = multiply(kTurn, j), sum1 = multiply(kTurn + 1, j);
-        add(kTurn, j, sum0, b_now);
-        add(kTurn + 1, j, sum1, b_now);
-      }
-      if (j % 2 == 0) load_in_row(kTurn + j / 2, more2, s, after);
-      read_matrix((s + 1) & 1, next, j);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    read_rows(next);
+    for (int i = 0; i < TM; ++i) scale[kSet][i] = row_scale(slot, i);
   }
   // Each SIMD has one of the first four waves and one of the others; the former
   // load in the first half of the rows, the latter in the second.  A load holds
@@ -252,20 +259,12 @@ struct Fp8Gemm {
     const int n = (row - kHalf) * kPieces;
     return n < kLoads ? n : kLoads;
   }
-  static_assert(TN == 4 && TM % 2 == 0, "the last two rows go in four columns");
   __device__ __forceinline__ void load_in_row(int i, bool more2, int s, uint32_t slot) const {
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
       const int j = i % kHalf * kPieces + n;
       if (more2 && turn == i / kHalf && j < kLoads) load_piece(s + 2, slot, j);
     }
-  }
-  static constexpr int kYoung = 4 + TM;
-  __device__ __forceinline__ void read_rows(uint32_t slot) {
-    af[0] = row_fragment(slot, 0);
-    af[1] = row_fragment(slot, 1);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) scale[i] = row_scale(slot, i);
   }
 
   __device__ __forceinline__ void accumulate() {
@@ -287,16 +286,17 @@ struct Fp8Gemm {
     else wait_loads<0>();
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) read_matrix(0, 0, j);
-    read_rows(0);
+    for (int j = 0; j < TN; ++j) read_matrix<0>(0, 0, j);
+    af[0] = row_fragment(0, 0);
+    af[1] = row_fragment(0, 1);
+    read_scales<0>(0);
     // (past the last stage, fragments are read from a slot that nobody uses)
-    uint32_t now = 0, next = 1, after = 2;
-    for (int s = 0; s < stages; ++s) {
-      step(s, now, next, after);
-      const uint32_t free = now;
-      now = next;
-      next = after;
-      after = free;
+    uint32_t slot = 0;
+    for (int s = 0; s < stages; s += 2) {
+      const uint32_t one = slot == 2 ? 0 : slot + 1, two = one == 2 ? 0 : one + 1;
+      step<0>(s, slot, one, two);
+      if (s + 1 < stages) step<1>(s + 1, one, two, slot);
+      slot = two;
     }
   }
 
