@@ -281,12 +281,13 @@ enum Mode { kForward = 0, kRowsGrad = 1, kWeightsGrad = 2 };
 template <int kMode, bool kF16, bool kGlu, int TM, int TN, int WM, int WN, int kWaveBytes>
 struct TileStore {
   static constexpr int kWaveCols = 16 * TN;
+  static constexpr int kMask = 4 * TN < 16 ? 4 * TN - 1 : 15;  // 16-byte chunks of a row that change places
   static constexpr int kOutCols = kWaveCols * WN / (kGlu && kMode == kForward ? 2 : 1);
 
   // A wave hands its results to itself through its quarter of the ring, so that
   // a lane gets 8 neighbouring columns of a row, neighbouring lanes the next
   // ones, and every store covers whole cache lines.  16-byte chunk c of row r
-  // lies at c ^ (r & 15): the 16 rows that one store instruction writes at the
+  // lies at c ^ (r & 15) (as far as the row has chunks): the 16 rows that one store instruction writes at the
   // same column touch every bank once.
   static constexpr int kFit = kWaveBytes / (16 * kWaveCols * 4);  // blocks of rows that fit at once
   static constexpr int pass_blocks() {  // the largest part of TM that fits
@@ -316,8 +317,8 @@ struct TileStore {
   }
   static __device__ __forceinline__ void fetch8(const char* own, int row, int col, float* v) {
     const int c = col >> 2;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(own + row * (kWaveCols * 4) + ((c ^ (row & 15)) << 4));
-    const f32x4 b = *reinterpret_cast<const f32x4*>(own + row * (kWaveCols * 4) + (((c + 1) ^ (row & 15)) << 4));
+    const f32x4 a = *reinterpret_cast<const f32x4*>(own + row * (kWaveCols * 4) + ((c ^ (row & kMask)) << 4));
+    const f32x4 b = *reinterpret_cast<const f32x4*>(own + row * (kWaveCols * 4) + (((c + 1) ^ (row & kMask)) << 4));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = a[k];
@@ -349,7 +350,7 @@ struct TileStore {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const int row = i * 16 + (lane & 15), c = j * 4 + (lane >> 4);
-          *reinterpret_cast<f32x4*>(own + row * (kWaveCols * 4) + ((c ^ (row & 15)) << 4)) =
+          *reinterpret_cast<f32x4*>(own + row * (kWaveCols * 4) + ((c ^ (row & kMask)) << 4)) =
               acc[pass * kPassBlocks + i][j];
         }
 #pragma unroll 4

@@ -15,7 +15,8 @@
 // it is the price of the instructions that work at twice the 16-bit rate.
 //
 // A workgroup of 8 waves makes a tile of 192 rows and 256 columns, 96 x 64 to a
-// wave (with fp32 scales the sums pass through vector instructions, so a wave
+// wave (64 x 128, 32 x 32 to a wave, where that is too much for the rows there are;
+// with fp32 scales the sums pass through vector instructions, so a wave
 // must hold them in vector registers).  A stage is 128 channels.  While the
 // matrix instructions work on stage s, both operands of stage s + 2 come in: LDS
 // holds three stages of rows (and all scales), and two of the matrix operand,
@@ -39,12 +40,12 @@ struct Fp8Gemm {
   static_assert(WM * WN == kWaves, "eight waves");
   static constexpr int kRows = 16 * TM * WM, kCols = 16 * TN * WN, kWaveCols = 16 * TN;
   static constexpr int kABytes = kRows * kStage, kBBytes = kCols * kStage;
-  static constexpr int kScaleBytes = (256 + kCols) * 4;  // one word per row of both operands
+  static constexpr int kScaleBytes = 2 * 256 * 4;  // one word per row of both operands
   static constexpr int kBAt = kASlots * kABytes, kScalesAt = kBAt + kBSlots * kBBytes;
   static constexpr int kLdsBytes = kScalesAt + kASlots * kScaleBytes;
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
-  static_assert(kBLoads == 4 && kWaveCols % 64 == 0, "a wave loads half of a wave's columns");
-  static_assert(kRows <= 256 && kRows % 64 == 0 && kCols == 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
+  static_assert(kBLoads * 8 == kWaveCols / 2, "a wave loads half of a wave's columns");
+  static_assert(kRows <= 256 && kCols <= 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
   static constexpr int kWaveBytes = kScalesAt / kWaves / 1024 * 1024;
   typedef TileStore<kForward, false, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
@@ -88,7 +89,7 @@ struct Fp8Gemm {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
     wn = wave % WN;
-    turn = wave / 4;
+    turn = kTurns == 2 ? wave / 4 : 0;
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
     stages = g.reduce / kStage;
     blocks = __builtin_amdgcn_readfirstlane(((t.rows + 15) / 16 - wm + WM - 1) / WM);
@@ -104,7 +105,9 @@ struct Fp8Gemm {
     // (a wave's 32 rows of the matrix operand are neighbours in memory too: of 32
     // rows all exist or none, as the columns are a multiple of 128)
     const int row = wave * kBLoads * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-    b_off[0] = (uint32_t)matrix_row(row) * (uint32_t)g.ldb + chunk * 16;
+    const int wave_row = matrix_row(wave * kBLoads * 8);
+    b0 += (int64_t)wave_row * g.ldb;
+    b_off[0] = (uint32_t)(matrix_row(row) - wave_row) * (uint32_t)g.ldb + chunk * 16;
     b_off[1] = b_off[0] ^ 64;
     const int q = lane >> 4, m = lane & 15;
     const uint32_t in_row = m * kStage + ((q ^ ((m >> 1) & 7)) << 4);
@@ -117,7 +120,7 @@ struct Fp8Gemm {
     if (kMx && wave >= 4) {
       s0 = bs0;
       s_step = 4;
-      s_off = (uint32_t)matrix_row(p) * (uint32_t)(g.ldb / 32);
+      s_off = (uint32_t)matrix_row(min(p, kCols - 1)) * (uint32_t)(g.ldb / 32);
     } else {
       s0 = static_cast<const char*>(g.a_scales) + t.row0 * g.a_scale_row * 4;
       s_step = g.a_scale_step * 4;
@@ -220,15 +223,15 @@ struct Fp8Gemm {
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+      load_in_row(i, more2, s, after);
       if (i == kTurn) {
         // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
         if (!more2) wait_loads<0>();
-        else if (turn == 0) wait_loads<kLoads>();
-        else wait_loads<issued_late(kTurn)>();
+        else if (turn == 0) wait_loads<issued(kTurn, 0)>();
+        else wait_loads<issued(kTurn, 1)>();
         lds_barrier<15>();
         read_scales<1 - kSet>(next);
       }
-      load_in_row(i, more2, s, after);
       const int f = i + 2;
       af[(2 * kSet + f) % kRing] = f < TM ? row_fragment(now, f) : row_fragment(next, f - TM);
       if (i == kTurn) {
@@ -254,10 +257,12 @@ struct Fp8Gemm {
   // load in the first half of the rows, the latter in the second.  A load holds
   // its wave until the address unit has taken it (16 cycles each, one unit for
   // all waves), and only the other wave keeps the matrix unit busy then.
+  // (Tiles of two row blocks a wave are for streaming the matrix: all load at once.)
+  static constexpr int kTurns = TM > 2 ? 2 : 1;
   static constexpr int kHalf = TM / 2, kPieces = (kLoads + kHalf - 1) / kHalf;
-  static constexpr int issued_late(int row) {
-    const int n = (row - kHalf) * kPieces;
-    return n < kLoads ? n : kLoads;
+  static constexpr int issued(int row, int turn) {  // loads of a wave when it has been through `row`
+    const int n = (row + 1 - turn * kHalf) * kPieces;
+    return n < 0 ? 0 : n < kLoads ? n : kLoads;
   }
   __device__ __forceinline__ void load_in_row(int i, bool more2, int s, uint32_t slot) const {
 #pragma unroll
@@ -311,7 +316,7 @@ struct Fp8Gemm {
 };
 
 template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, 2) void gemm_fp8_kernel(GemmArgs g) {
+__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_fp8_kernel(GemmArgs g) {
   typedef Fp8Gemm<kMx, kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
@@ -331,10 +336,33 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
 
 }  // namespace
 
+// Tiles of 64 x 128, two workgroups to a CU, where the big ones would leave the
+// GPU waiting: experts of few rows, whose products read the matrix and little
+// else (more loads in flight), and products with so few tiles that all of the
+// small ones run at once (a stage takes a small tile half the time).  Measured
+// with 7168 channels, small against large, us with fp32 / E8M0 scales:
+//   256 experts, 1024 columns, 2 rows each        270 / 324 against 312 / 359
+//   the same, 16 rows                             322 / 381 against 328 / 378
+//   the same, 32 rows                             349 / 413 against 340 / 394
+//   the same, 64 rows                             507 / 585 against 372 / 426
+//   1 expert, 4096 columns, 64 rows                34 /  33 against  63 /  60
+//   the same, 1024 rows (512 small tiles)          54 /  62 against  88 /  76
+//   the same, 2048 rows (1024)                    106 / 116 against  97 /  82
+//   8 experts, 4096 columns, 128 rows each (512)   58 /  65 against  82 /  72
+//   the same, 256 rows each (1024)                117 / 139 against  97 /  93
+template <bool kMx, bool kGlu>
+hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
+  const RowGroups& r = g.groups;
+  const int64_t groups = r.wanted > r.E ? r.E : r.wanted, rows = (r.wanted + r.E - 1) / r.E;
+  const int64_t columns = (int64_t)g.out_cols * (kGlu ? 2 : 1);
+  const bool small = rows <= 16 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
+  return small ? launch<kMx, kGlu, 2, 2, 2, 4>(g, stream) : launch<kMx, kGlu, 6, 4, 2, 4>(g, stream);
+}
+
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream) {
   const bool glu = g.act == EP_ACT_SWIGLU;
-  if (mx) return glu ? launch<true, true, 6, 4, 2, 4>(g, stream) : launch<true, false, 6, 4, 2, 4>(g, stream);
-  return glu ? launch<false, true, 6, 4, 2, 4>(g, stream) : launch<false, false, 6, 4, 2, 4>(g, stream);
+  if (mx) return glu ? launch_size<true, true>(g, stream) : launch_size<true, false>(g, stream);
+  return glu ? launch_size<false, true>(g, stream) : launch_size<false, false>(g, stream);
 }
 
 }  // namespace ep
