@@ -150,10 +150,15 @@ struct TileGemm {
       if constexpr (kAContig) a_off[i] = (uint32_t)min(row, a_limit - 1) * (uint32_t)g.lda * 2u + chunk * 16;
       else a_off[i] = (uint32_t)row * (uint32_t)g.lda * 2u + min(chunk * 8, a_limit - 8) * 2;
     }
+    // A wave's rows of the matrix operand are neighbours in memory (all gates, or
+    // all ups): offsets count from their first.
+    static_assert(!kBContig || kWaveCols / 2 % (B::kLoads * 8) == 0, "a wave loads gates or ups");
+    const int wave_row = kBContig ? matrix_row(wave * B::kLoads * 8) : 0;
+    if constexpr (kBContig) b0 += (int64_t)wave_row * g.ldb * 2;
 #pragma unroll
     for (int i = 0; i < B::kLoads; ++i) {
       const int row = B::load_row(i), chunk = B::load_chunk(i);
-      if constexpr (kBContig) b_off[i] = (uint32_t)matrix_row(row) * (uint32_t)g.ldb * 2u + chunk * 16;
+      if constexpr (kBContig) b_off[i] = (uint32_t)(matrix_row(row) - wave_row) * (uint32_t)g.ldb * 2u + chunk * 16;
       else b_off[i] = (uint32_t)row * (uint32_t)g.ldb * 2u + min(chunk * 8, b_limit - 8) * 2;
     }
     a_step = kAContig ? kUnit * 2 : (int64_t)kUnit * g.lda * 2;
@@ -486,14 +491,21 @@ hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, h
   return f16 ? launch_mode<true>(g, mode, large, stream) : launch_mode<false>(g, mode, large, stream);
 }
 
-// Which kernel.  Few rows: tiles of 128 x 128 stream the matrix at 6.1 TB/s if
-// there are enough of them, but one tile takes 0.55 us for every 64 of the
-// reduction, however few there are; the kernel for few rows fills the GPU from
-// 4096 columns on, and reads a once for every 16 columns.  Measured with a
-// reduction of 7168, few against tiles: 16 rows, 4096 columns (32 tiles) 19
-// against 89 us, 16,384 columns (128 tiles) 53 against 62; 64 experts of 16 rows
-// and 2048 columns (1024 tiles) 617 against 313; 64 rows, 16,384 columns 167
-// against 65.  Hence its limit of 128 tiles, fewer for more rows.
+// Which kernel.  Tiles of 128 x 128 stream the matrix at 6.1 TB/s if there are
+// enough of them, but one tile takes 0.6 us for every 64 of the reduction, however
+// few there are.  So where there are few, the kernels whose waves share out the
+// reduction are faster: 16 matrix rows to a workgroup fill the GPU from 4096
+// columns on, but read a once for every 16 columns; 64 x 64 tiles are right up to
+// one for every CU.  Measured, us, by 16 columns / 64 x 64 / 128 x 128:
+//   reduction 7168: 16 rows, 4096 columns    13 /  31 /  89
+//                   64 rows, 4096 columns    22 /  33 /  91
+//                   256 rows, 4096 columns      /  40 /  72 (256 tiles of 64 x 64)
+//                   512 rows, 4096 columns      /  77 /  73
+//   reduction 4096: 16 rows, 16,384 columns  28 /  24 /
+//                   64 rows, 16,384 columns  50 /  27 /  39
+//   reduction 2048: 1024 rows, 1024 columns     /  15 /  25 (256)
+//                   2048 rows, 1024 columns     /  28 /  26
+//   reduction 2048, 32 experts of 1024 columns: 16 rows each (512) 41 / 29 / 24
 // Otherwise 256 x 256 tiles where the groups have the rows for them and there
 // are enough tiles for every CU.
 hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream) {
@@ -502,7 +514,9 @@ hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream
   const int64_t groups = mode == kWeightsGrad || r.wanted > r.E ? r.E : r.wanted;
   const int64_t columns = (int64_t)g.out_cols * (mode == kForward && g.act == EP_ACT_SWIGLU ? 2 : 1);
   if (mode == kForward && rows <= 64 && groups * ((columns + 127) / 128) * ((rows + 15) / 16) <= 128)
-    return launch_gemm_few(g, rows, f16, stream);
+    return launch_gemm_few(g, rows, false, f16, stream);
+  if (mode == kForward && groups * ((rows + 63) / 64) * ((columns + 63) / 64) <= kChipCUs)
+    return launch_gemm_few(g, rows, true, f16, stream);
   const int64_t tiles = groups * ((rows + 255) / 256) * ((columns + 255) / 256);
   return launch_gemm_tile(g, mode, f16, rows >= 192 && tiles >= kChipCUs, stream);
 }

@@ -103,6 +103,50 @@ def test_expert_gemm_large_groups(name, T, K, N):
         check(out[b:b + n], act(z, "swiglu"), act_error(z, K * SUM * s, "swiglu"), "expert %d" % e)
 
 
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,k,E,cap,D,F", [(1500, 2, 6, 0, 136, 5440), (900, 2, 4, 500, 264, 8200)])
+def test_expert_products_in_large_tiles(name, T, k, E, cap, D, F):
+    """256 tiles of 256 x 256 and more, of every kind: up with a bias, its gradients by rows and by
+    weights (adding to what was there, and in the operands' type)."""
+    note("large tiles", name, T, k, E, cap, D, F)
+    dtype, dt = TYPES[name]
+    g = gen(T)
+    lay = layout(T, k, E, cap, g, 0.05, cap > 0)
+    R, used = lay.num_recv_rows, used_rows(lay)
+    x, w, bias = randn((R, D), dt, g), randn((E, 2 * F, D), dt, g, D ** -0.5), randn((E, 2 * F), dt, g)
+    dy, back, pre_in = randn((R, D), dt, g), randn((E, D, F), dt, g, D ** -0.5), randn((R, 2 * F), dt, g)
+    x[~used] = float("nan")
+    dy[~used] = float("inf")
+    out, pre = (torch.full((R, n), 7.0, dtype=dt, device="cuda") for n in (F, 2 * F))
+    B.ep_expert_gemm(x, w, lay, out, dtype, act=B.EP_ACT_SWIGLU, bias=bias, preact=pre)
+    dx = torch.full((R, 2 * F), 7.0, dtype=dt, device="cuda")
+    B.ep_expert_gemm_grad_x(dy, back, lay, dx, dtype, act=B.EP_ACT_SWIGLU, preact=pre_in)
+    wide = randn((R, 2 * F), dt, g)
+    wide[~used] = float("nan")
+    dw, db = torch.full((E, 2 * F, D), 7.0, dtype=dt, device="cuda"), torch.full((E, 2 * F), 7.0, dtype=dt, device="cuda")
+    B.ep_expert_gemm_grad_w(wide, x, lay, dw, dtype, dbias=db)
+    old = randn((E, D, 2 * F), torch.float32, g)
+    acc = old.clone()
+    B.ep_expert_gemm_grad_w(x, wide, lay, acc, dtype | B.EP_GRAD_F32 | B.EP_GRAD_ACCUMULATE)
+    torch.cuda.synchronize()
+    for t in (out, pre, dx):
+        assert (t[~used] == 7).all()
+    for e, (b, n) in enumerate(segments(lay)):
+        xe, ye, we, v = x[b:b + n].double(), wide[b:b + n].double(), w[e].double(), back[e].double()
+        z, m = xe @ we.T + bias[e].double(), xe.abs() @ we.abs().T + bias[e].double().abs()
+        dz = (D + 1) * SUM * m
+        check(pre[b:b + n], z, dz, "preact of expert %d" % e)
+        check(out[b:b + n], act(z, "swiglu"), act_error(z, dz, "swiglu"), "out of expert %d" % e)
+        de, p = dy[b:b + n].double(), pre_in[b:b + n].double()
+        d, dd = de @ v, D * SUM * (de.abs() @ v.abs())
+        check(dx[b:b + n], act_grad(d, p, "swiglu"), act_grad_error(d, dd, p, "swiglu"), "dx of expert %d" % e)
+        ref, m = ye.T @ xe, ye.abs().T @ xe.abs()
+        check(dw[e], ref, n * SUM * m, "dweights of expert %d" % e)
+        check(db[e], ye.sum(0), n * SUM * ye.abs().sum(0), "dbias of expert %d" % e)
+        o = old[e].double()
+        check(acc[e], o + ref.T, (n + 1) * SUM * (m.T + o.abs()), "accumulated dweights of expert %d" % e)
+
+
 # ------------------------------------------------------------------------------------- FP8
 def quant_rows(x, block):
     """E4M3 codes and per-block scales of rows: fp32 per 128, or E8M0 per 32 (with widely spread scales)."""
@@ -123,7 +167,10 @@ def codes(q):
 @pytest.mark.parametrize("kind", ["fp8", "pow2", "mn", "mxfp8"])
 @pytest.mark.parametrize("a,bias", [("none", True), ("swiglu", False), ("gelu", True)])
 @pytest.mark.parametrize("T,k,E,cap,K,N", [(37, 3, 5, 0, 128, 128), (50, 4, 8, 9, 640, 256),
-                                             (3, 2, 70, 0, 256, 128), (900, 1, 2, 0, 384, 384)])
+                                             (3, 2, 70, 0, 256, 128), (900, 1, 2, 0, 384, 384),
+                                             # few rows on average, many for some; large tiles
+                                             (400, 2, 70, 0, 256, 640), (900, 1, 2, 0, 384, 2304),
+                                             (700, 2, 3, 300, 640, 4608), (1500, 1, 1, 0, 128, 2944)])
 def test_expert_gemm_fp8(kind, a, bias, T, k, E, cap, K, N):
     note("fp8", kind, a, T, k, E, cap, K, N)
     g = gen(T + K)
@@ -303,7 +350,12 @@ def test_neighbours_infinities_stay_with_their_expert():
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 @pytest.mark.parametrize("a", list(ACTS))
 @pytest.mark.parametrize("T,K,N", [(1, 64, 64), (3, 1032, 24), (16, 8, 8), (17, 520, 264), (64, 2048, 40),
-                                     (129, 72, 136), (300, 256, 520)])
+                                     (129, 72, 136), (300, 256, 520),
+                                     # chunks that go round every ring, rows at the block edges
+                                     (15, 4616, 40), (32, 4616, 24), (33, 4616, 136), (63, 584, 72),
+                                     (65, 1544, 72), (200, 2056, 200),
+                                     # 128 x 128 and 256 x 256 tiles
+                                     (130, 200, 5640), (2100, 136, 7240), (2304, 72, 7424)])
 def test_linear(name, a, T, K, N):
     note("linear", name, a, T, K, N)
     dtype, dt = TYPES[name]
@@ -334,7 +386,8 @@ def test_linear(name, a, T, K, N):
 
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 @pytest.mark.parametrize("a", list(ACTS))
-@pytest.mark.parametrize("T,K,N", [(1, 64, 64), (5, 24, 1032), (17, 264, 520), (300, 520, 256), (0, 64, 72)])
+@pytest.mark.parametrize("T,K,N", [(1, 64, 64), (5, 24, 1032), (17, 264, 520), (300, 520, 256), (0, 64, 72),
+                                     (2100, 7240, 200), (200, 7240, 2104)])
 def test_linear_gradients(name, a, T, K, N):
     note("linear grads", name, a, T, K, N)
     dtype, dt = TYPES[name]
@@ -452,3 +505,42 @@ def test_combine_grad(name, T, k, E, cap, H, masked):
     only = torch.full((R, H), 7.0, dtype=dt, device="cuda")
     B.ep_combine_grad(dout, None, w, lay, only, None, dtype)
     assert torch.equal(only, dy)
+
+
+# ------------------------------------------------------------------- matrices beyond 2^32 bytes
+@pytest.mark.parametrize("T", [3, 200])
+def test_linear_offsets_past_32_bits(T):
+    """A swiglu product whose ups begin 4 GiB into the matrix and whose last rows lie past 8 GiB:
+    columns from both ends against 64 bits (few rows and many take different kernels)."""
+    note("past 32 bits", T)
+    dtype, dt, K, N = B.EP_BF16, torch.bfloat16, 32768, 65536
+    g = gen(T)
+    x = randn((T, K), dt, g)
+    w = torch.empty((2 * N, K), dtype=dt, device="cuda").normal_(0, K ** -0.5, generator=g)
+    out, pre = torch.zeros((T, N), dtype=dt, device="cuda"), torch.zeros((T, 2 * N), dtype=dt, device="cuda")
+    B.ep_linear(x, w, out, dtype, act=B.EP_ACT_SWIGLU, preact=pre)
+    cols = torch.tensor([0, 1, 17, N // 2 - 1, N // 2, N - 129, N - 1], device="cuda")
+    both = torch.cat([cols, cols + N])
+    z, m = x.double() @ w[both].double().T, x.double().abs() @ w[both].double().abs().T
+    dz = K * SUM * m
+    check(pre[:, both], z, dz, "preact")
+    check(out[:, cols], act(z, "swiglu"), act_error(z, dz, "swiglu"), "out")
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_expert_gemm_fp8_offsets_past_32_bits(T):
+    note("fp8 past 32 bits", T)
+    K, N = 65536, 65536
+    g = gen(T)
+    lay = B.EpLayout(T, 1, 1, 1)
+    B.ep_get_layout(torch.zeros((T, 1), dtype=torch.int64, device="cuda"), lay)
+    q, s = quant_rows(torch.randn((T, K), device="cuda", generator=g), 128)
+    w = torch.randint(0, 0x60, (1, 2 * N, K), dtype=torch.uint8, device="cuda", generator=g)
+    ws = torch.full((1, 2 * N // 128, K // 128), 2.0 ** -8, device="cuda")
+    out, pre = (torch.zeros((T, n), dtype=torch.bfloat16, device="cuda") for n in (N, 2 * N))
+    B.ep_expert_gemm(q, w, lay, out, B.EP_FP8_E4M3, act=B.EP_ACT_SWIGLU, x_scales=s, weight_scales=ws, preact=pre)
+    cols = torch.tensor([0, 130, N // 2, N - 1], device="cuda")
+    both = torch.cat([cols, cols + N])
+    xd, wd = codes(q) * s.double().repeat_interleave(128, 1), codes(w[0, both]) * 2.0 ** -8
+    z, m = xd @ wd.T, xd.abs() @ wd.abs().T
+    check(pre[:, both], z, (K + 4) * SUM * m + fp8_group_error(xd, wd), "preact")
