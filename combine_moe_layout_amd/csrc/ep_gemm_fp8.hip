@@ -35,14 +35,18 @@ constexpr int kASlots = 3;  // stages of rows and of scales in LDS
 constexpr int kBSlots = 2;  // stages of the matrix operand
 constexpr int kStage = 128;  // channels, and bytes, per stage
 
-template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
+template <bool kMx, bool kGlu, bool kQuad, int TM, int TN, int WM, int WN>
 struct Fp8Gemm {
   static_assert(WM * WN == kWaves, "eight waves");
   static constexpr int kRows = 16 * TM * WM, kCols = 16 * TN * WN, kWaveCols = 16 * TN;
   static constexpr int kABytes = kRows * kStage, kBBytes = kCols * kStage;
-  static constexpr int kScaleBytes = 2 * 256 * 4;  // one word per row of both operands
+  // Scales: one word per row of both operands and stage; kQuad: four stages' words
+  // at once (a load of one word from each of 64 rows costs the address unit as much
+  // as the 64 lines that it touches).
+  static constexpr int kScaleSlots = kQuad ? 2 : 3, kScalePitch = kQuad ? 16 : 4;
+  static constexpr int kScaleBytes = 2 * 256 * kScalePitch;
   static constexpr int kBAt = kASlots * kABytes, kScalesAt = kBAt + kBSlots * kBBytes;
-  static constexpr int kLdsBytes = kScalesAt + kASlots * kScaleBytes;
+  static constexpr int kLdsBytes = kScalesAt + kScaleSlots * kScaleBytes;
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
   static_assert(kBLoads * 8 == kWaveCols / 2, "a wave loads half of a wave's columns");
   static_assert(kRows <= 256 && kCols <= 256, "scale words: waves 0 to 3 bring the rows', 4 to 7 the columns'");
@@ -119,36 +123,44 @@ struct Fp8Gemm {
     bs0 = static_cast<const char*>(g.b_scales) + t.e * (kMx ? g.b_stride / 32 : g.b_stride / (128 * 128) * 4);
     if (kMx && wave >= 4) {
       s0 = bs0;
-      s_step = 4;
+      s_step = kScalePitch;
       s_off = (uint32_t)matrix_row(min(p, kCols - 1)) * (uint32_t)(g.ldb / 32);
     } else {
       s0 = static_cast<const char*>(g.a_scales) + t.row0 * g.a_scale_row * 4;
-      s_step = g.a_scale_step * 4;
+      s_step = kQuad ? 16 : g.a_scale_step * 4;
       s_off = (uint32_t)(min(p, t.rows - 1) * g.a_scale_row * 4);
     }
-    as_read = kScalesAt + (wm * 16 + m) * 4 + (kMx ? q : 0);
-    bs_read = kScalesAt + 256 * 4 + (wn * kWaveCols + m) * 4 + q;
+    as_read = kScalesAt + (wm * 16 + m) * kScalePitch + (kMx ? q : 0);
+    bs_read = kScalesAt + (256 + wn * kWaveCols + m) * kScalePitch + q;
     // The wave's columns (32 gates and 32 ups, or 64) lie in one block of 128 each.
     const int64_t per_row = g.ldb / 128;
     block0 = (uint32_t)(matrix_row(wn * kWaveCols) / 128 * per_row);
     block1 = (uint32_t)(matrix_row(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
   }
 
-  // Load j of stage s: of the row operand (into slot `slot`), of the scales, of
-  // the matrix operand.
-  static constexpr int kLoads = kALoads + 1 + kBLoads;
+  // Load j of stage s: of the row operand (into slot `slot`), of the matrix
+  // operand, of the scales.
+  static constexpr int kLoads = kALoads + kBLoads + (kQuad ? 0 : 1);
   __device__ __forceinline__ void load_piece(int s, uint32_t slot, int j) const {
     if (j < kALoads) {
       load16_to_lds(a0 + s * kStage, a_off[j < kALoads ? j : 0],
                     lds0 + slot * kABytes + (wave * kALoads + j) * 1024);
-    } else if (j == kALoads) {
-      load4_to_lds(s0 + s * s_step, s_off,
-                   lds0 + kScalesAt + slot * kScaleBytes + (kMx ? wave : wave & 3) * 256);
-    } else {
-      const int i = j - kALoads - 1;
+    } else if (j < kALoads + kBLoads) {
+      const int i = j - kALoads;
       load16_to_lds(b0 + s * kStage + (int64_t)i * 8 * g.ldb, b_off[i & 1],
                     lds0 + kBAt + (s & 1) * kBBytes + (wave * kBLoads + i) * 1024);
+    } else {
+      load4_to_lds(s0 + s * s_step, s_off, lds0 + kScalesAt + slot * kScaleBytes + (kMx ? wave : wave & 3) * 256);
     }
+  }
+  // kQuad: the scales of stages s .. s + 3 (s a multiple of 4).
+  __device__ __forceinline__ void load_quad(int s) const {
+    load16_to_lds(s0 + (s >> 2) * s_step, s_off,
+                  lds0 + kScalesAt + ((s >> 2) & 1) * kScaleBytes + (kMx ? wave : wave & 3) * 1024);
+  }
+  // Where stage s's scales begin, its rows being in slot `slot`.
+  __device__ __forceinline__ uint32_t scales_at(int s, uint32_t slot) const {
+    return kQuad ? ((s >> 2) & 1) * kScaleBytes + (s & 3) * 4 : slot * kScaleBytes;
   }
 
   // Lane 16 q + m holds channels 16 q .. 16 q + 15 and 64 + 16 q .. of row m
@@ -163,10 +175,10 @@ struct Fp8Gemm {
     return read_fragment(slot * kABytes + a_read + i * (WM * 16 * kStage));
   }
   template <int kSet>
-  __device__ __forceinline__ void read_matrix(uint32_t b_slot, uint32_t slot, int j) {
+  __device__ __forceinline__ void read_matrix(uint32_t b_slot, uint32_t scales, int j) {
     bf[kSet][j] = read_fragment(b_slot * kBBytes + b_read + j * (16 * kStage));
     if constexpr (kMx)
-      b_byte[kSet][j] = *reinterpret_cast<const uint8_t*>(lds + slot * kScaleBytes + bs_read + j * 64);
+      b_byte[kSet][j] = *reinterpret_cast<const uint8_t*>(lds + scales + bs_read + j * 16 * kScalePitch);
   }
   // A block's fp32 scale, by a scalar load (it must not wait for the loads to LDS).
   __device__ __forceinline__ float block_scale(uint32_t index, int s) const {
@@ -196,9 +208,9 @@ struct Fp8Gemm {
       for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(sum[k], f, acc[i][j][k]);
     }
   }
-  // Row block i's scale in slot `slot`: the E8M0 byte of this lane's 32 channels, or the fp32 bits.
-  __device__ __forceinline__ int32_t row_scale(uint32_t slot, int i) const {
-    const char* at = lds + slot * kScaleBytes + as_read + i * (WM * 64);
+  // Row block i's scale: the E8M0 byte of this lane's 32 channels, or the fp32 bits.
+  __device__ __forceinline__ int32_t row_scale(uint32_t scales, int i) const {
+    const char* at = lds + scales + as_read + i * (WM * 16 * kScalePitch);
     if constexpr (kMx) return *reinterpret_cast<const uint8_t*>(at);
     else return *reinterpret_cast<const int32_t*>(at);
   }
@@ -214,6 +226,9 @@ struct Fp8Gemm {
     // stage's second row fragment).
     lds_barrier<2>();
     const bool more = s + 1 < stages, more2 = s + 2 < stages;
+    const bool quad = kQuad && more2 && ((s + 2) & 3) == 0;
+    if (quad) load_quad(s + 2);
+    const uint32_t scales = scales_at(s + 1, next);
     const float b_now[2] = {b_scale[0], b_scale[1]};
     if constexpr (!kMx) {
       if (more) {
@@ -227,16 +242,18 @@ struct Fp8Gemm {
       if (i == kTurn) {
         // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
         if (!more2) wait_loads<0>();
+        else if (quad && turn == 0) wait_loads<issued(kTurn, 0) + 1>();
+        else if (quad) wait_loads<issued(kTurn, 1) + 1>();
         else if (turn == 0) wait_loads<issued(kTurn, 0)>();
         else wait_loads<issued(kTurn, 1)>();
         lds_barrier<15>();
-        read_scales<1 - kSet>(next);
+        read_scales<1 - kSet>(scales);
       }
       const int f = i + 2;
       af[(2 * kSet + f) % kRing] = f < TM ? row_fragment(now, f) : row_fragment(next, f - TM);
       if (i == kTurn) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) read_matrix<1 - kSet>((s + 1) & 1, next, j);
+        for (int j = 0; j < TN; ++j) read_matrix<1 - kSet>((s + 1) & 1, scales, j);
       }
       if (i < blocks) {
         f32x4 sum[TN];
@@ -249,9 +266,9 @@ struct Fp8Gemm {
     }
   }
   template <int kSet>
-  __device__ __forceinline__ void read_scales(uint32_t slot) {
+  __device__ __forceinline__ void read_scales(uint32_t scales) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) scale[kSet][i] = row_scale(slot, i);
+    for (int i = 0; i < TM; ++i) scale[kSet][i] = row_scale(scales, i);
   }
   // Each SIMD has one of the first four waves and one of the others; the former
   // load in the first half of the rows, the latter in the second.  A load holds
@@ -279,6 +296,7 @@ struct Fp8Gemm {
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) load_piece(0, 0, j);
+    if constexpr (kQuad) load_quad(0);
     if (stages > 1) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) load_piece(1, 1, j);
@@ -315,22 +333,22 @@ struct Fp8Gemm {
   }
 };
 
-template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
+template <bool kMx, bool kGlu, bool kQuad, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_fp8_kernel(GemmArgs g) {
-  typedef Fp8Gemm<kMx, kGlu, TM, TN, WM, WN> G;
+  typedef Fp8Gemm<kMx, kGlu, kQuad, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
   gemm.run();
 }
 
-template <bool kMx, bool kGlu, int TM, int TN, int WM, int WN>
+template <bool kMx, bool kGlu, bool kQuad, int TM, int TN, int WM, int WN>
 hipError_t launch(const GemmArgs& g, hipStream_t stream) {
-  typedef Fp8Gemm<kMx, kGlu, TM, TN, WM, WN> G;
+  typedef Fp8Gemm<kMx, kGlu, kQuad, TM, TN, WM, WN> G;
   const int64_t ct = (g.out_cols + G::kOutCols - 1) / G::kOutCols;
   const int64_t blocks = (max_row_tiles(g.groups, G::kRows) * ct + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  gemm_fp8_kernel<kMx, kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g);
+  gemm_fp8_kernel<kMx, kGlu, kQuad, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g);
   return hipGetLastError();
 }
 
@@ -350,19 +368,28 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
 //   the same, 2048 rows (1024)                    106 / 116 against  97 /  82
 //   8 experts, 4096 columns, 128 rows each (512)   58 /  65 against  82 /  72
 //   the same, 256 rows each (1024)                117 / 139 against  97 /  93
-template <bool kMx, bool kGlu>
+template <bool kMx, bool kGlu, bool kQuad>
 hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const RowGroups& r = g.groups;
   const int64_t groups = r.wanted > r.E ? r.E : r.wanted, rows = (r.wanted + r.E - 1) / r.E;
   const int64_t columns = (int64_t)g.out_cols * (kGlu ? 2 : 1);
   const bool small = rows <= 16 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
-  return small ? launch<kMx, kGlu, 2, 2, 2, 4>(g, stream) : launch<kMx, kGlu, 6, 4, 2, 4>(g, stream);
+  return small ? launch<kMx, kGlu, kQuad, 2, 2, 2, 4>(g, stream) : launch<kMx, kGlu, kQuad, 6, 4, 2, 4>(g, stream);
+}
+
+// Four stages' scales at once where they lie in whole 16-byte words.
+template <bool kMx>
+hipError_t launch_scales(const GemmArgs& g, hipStream_t stream) {
+  const auto whole = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool quad = g.reduce % (4 * kStage) == 0 && g.a_scale_step == 1 && whole(g.a_scales) &&
+                    (!kMx || whole(g.b_scales));
+  if (g.act == EP_ACT_SWIGLU)
+    return quad ? launch_size<kMx, true, true>(g, stream) : launch_size<kMx, true, false>(g, stream);
+  return quad ? launch_size<kMx, false, true>(g, stream) : launch_size<kMx, false, false>(g, stream);
 }
 
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream) {
-  const bool glu = g.act == EP_ACT_SWIGLU;
-  if (mx) return glu ? launch_size<true, true>(g, stream) : launch_size<true, false>(g, stream);
-  return glu ? launch_size<false, true>(g, stream) : launch_size<false, false>(g, stream);
+  return mx ? launch_scales<true>(g, stream) : launch_scales<false>(g, stream);
 }
 
 }  // namespace ep

@@ -170,7 +170,10 @@ def codes(q):
                                              (3, 2, 70, 0, 256, 128), (900, 1, 2, 0, 384, 384),
                                              # few rows on average, many for some; large tiles
                                              (400, 2, 70, 0, 256, 640), (900, 1, 2, 0, 384, 2304),
-                                             (700, 2, 3, 300, 640, 4608), (1500, 1, 1, 0, 128, 2944)])
+                                             (700, 2, 3, 300, 640, 4608), (1500, 1, 1, 0, 128, 2944),
+                                             # scales four stages at a time
+                                             (37, 3, 5, 0, 512, 128), (50, 4, 8, 9, 2560, 256),
+                                             (900, 1, 2, 0, 512, 2304), (1500, 1, 1, 0, 2560, 2944)])
 def test_expert_gemm_fp8(kind, a, bias, T, k, E, cap, K, N):
     note("fp8", kind, a, T, k, E, cap, K, N)
     g = gen(T + K)
