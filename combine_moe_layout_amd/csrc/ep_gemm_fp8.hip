@@ -359,21 +359,20 @@ hipError_t launch(const GemmArgs& g, hipStream_t stream) {
 // else (more loads in flight), and products with so few tiles that all of the
 // small ones run at once (a stage takes a small tile half the time).  Measured
 // with 7168 channels, small against large, us with fp32 / E8M0 scales:
-//   256 experts, 1024 columns, 2 rows each        270 / 324 against 312 / 359
-//   the same, 16 rows                             322 / 381 against 328 / 378
-//   the same, 32 rows                             349 / 413 against 340 / 394
-//   the same, 64 rows                             507 / 585 against 372 / 426
-//   1 expert, 4096 columns, 64 rows                34 /  33 against  63 /  60
-//   the same, 1024 rows (512 small tiles)          54 /  62 against  88 /  76
-//   the same, 2048 rows (1024)                    106 / 116 against  97 /  82
-//   8 experts, 4096 columns, 128 rows each (512)   58 /  65 against  82 /  72
-//   the same, 256 rows each (1024)                117 / 139 against  97 /  93
+//   256 experts, 1024 columns, 2 rows each        301 / 312 against 314 / 323
+//   the same, 32 rows                             332 / 349 against 337 / 355
+//   the same, 64 rows                             436 / 465 against 361 / 375
+//   1 expert, 4096 columns, 64 rows                34 /  32 against  69 /  65
+//   the same, 1024 rows (512 small tiles)          55 /  51 against  92 /  80
+//   the same, 2048 rows (1024)                    107 /  98 against 100 /  83
+//   8 experts, 4096 columns, 128 rows each (512)   53 /  51 against  85 /  76
+//   the same, 256 rows each (1024)                106 / 108 against  97 /  86
 template <bool kMx, bool kGlu, bool kQuad>
 hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const RowGroups& r = g.groups;
   const int64_t groups = r.wanted > r.E ? r.E : r.wanted, rows = (r.wanted + r.E - 1) / r.E;
   const int64_t columns = (int64_t)g.out_cols * (kGlu ? 2 : 1);
-  const bool small = rows <= 16 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
+  const bool small = rows <= 32 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
   return small ? launch<kMx, kGlu, kQuad, 2, 2, 2, 4>(g, stream) : launch<kMx, kGlu, kQuad, 6, 4, 2, 4>(g, stream);
 }
 
