@@ -109,6 +109,10 @@ struct Tile {
 // skips a tile's blocks of 16 rows that it does not have).
 // Every wave does the search by itself: its lanes hold E/64 groups each.
 constexpr int kXcds = 8;
+// ceil(count / height); a count may be as large as 2^31 - 1.
+__device__ __forceinline__ int32_t tiles_of(int32_t count, int32_t height) {
+  return (int32_t)(((uint32_t)count + (uint32_t)height - 1) / (uint32_t)height);
+}
 __device__ __forceinline__ int64_t uniform(int64_t v) {  // the same in every lane: to scalar registers
   return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(v >> 32)) << 32) |
                    (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)v));
@@ -121,7 +125,7 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   int32_t mine = 0;
   for (int j = 0; j < per; ++j) {
     const int e = lane * per + j;
-    if (e < g.E) mine += (group_count(g, e) + height - 1) / height;
+    if (e < g.E) mine += tiles_of(group_count(g, e), height);
   }
   const int32_t incl = wave_inclusive_sum(mine);
   const int32_t row_tiles = __builtin_amdgcn_readlane(incl, 63);
@@ -143,7 +147,7 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   int32_t left = target - before, e = lane * per;
   for (int j = 0; j < per; ++j) {
     if (e >= g.E - 1) break;
-    const int32_t n = (group_count(g, e) + height - 1) / height;
+    const int32_t n = tiles_of(group_count(g, e), height);
     if (left < n) break;
     left -= n;
     ++e;
@@ -151,10 +155,9 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   t.e = __builtin_amdgcn_readlane(e, owner);
   left = __builtin_amdgcn_readlane(left, owner);
   const int32_t count = group_count(g, t.e);
-  const int32_t tiles = (count + height - 1) / height;
-  const int32_t even = ((count + tiles - 1) / tiles + 15) & ~15;
+  const int32_t even = (tiles_of(count, tiles_of(count, height)) + 15) & ~15;
   const int32_t each = min(height, even);
-  t.rows = min(each, count - left * each);
+  t.rows = (int32_t)min((int64_t)each, count - (int64_t)left * each);
   t.row0 = group_first(g, t.e) + (int64_t)left * each;
   t.rows = __builtin_amdgcn_readfirstlane(t.rows);
   t.row0 = uniform(t.row0);

@@ -547,3 +547,52 @@ def test_expert_gemm_fp8_offsets_past_32_bits(T):
     xd, wd = codes(q) * s.double().repeat_interleave(128, 1), codes(w[0, both]) * 2.0 ** -8
     z, m = xd @ wd.T, xd.abs() @ wd.abs().T
     check(pre[:, both], z, (K + 4) * SUM * m + fp8_group_error(xd, wd), "preact")
+
+
+def test_linear_rows_near_2_to_31():
+    """A tile count, height and first row that leave 32 bits on the way: rows from both ends."""
+    T, K, N = 2 ** 31 - 3001, 8, 8
+    if torch.cuda.mem_get_info()[0] < 90 * 2 ** 30:
+        pytest.skip("needs 70 GB")
+    note("rows near 2^31")
+    g = gen(3)
+    part = randn((4096, K), torch.bfloat16, g)
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    whole = T // 4096 * 4096
+    x[:whole].view(-1, 4096, K)[:] = part
+    x[whole:] = part[:T - whole]
+    w = randn((N, K), torch.bfloat16, g)
+    out = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+    B.ep_linear(x, w, out, B.EP_BF16)
+    for at in (0, 4096 * 3, 2 ** 30 // 8 * 8, whole - 4096 * 2, T - 4096):
+        xe = x[at:at + 4096].double()
+        check(out[at:at + 4096], xe @ w.double().T, K * SUM * (xe.abs() @ w.double().abs().T), "rows at %d" % at)
+    del x, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+@pytest.mark.parametrize("a", ["relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("T", [8, 400])
+def test_activations_over_the_whole_range(name, a, T):
+    """Arguments from the type's smallest to its largest magnitudes, forward and back.  Exponentials
+    past fp32's range end in 0 or infinity: up to 2^-80 absolute (|z| 2^-126 at |z| near 88)."""
+    note("whole range", name, a, T)
+    dtype, dt = TYPES[name]
+    g = gen(T)
+    N = 64
+    e = (30.0 if name == "bf16" else 12.0) * torch.rand((T, width(N, a)), device="cuda", generator=g) - 15.0
+    x = (torch.exp2(e) * torch.sign(torch.randn(e.shape, device="cuda", generator=g))).to(dt)
+    x[:, :8] = torch.tensor([0.0, -0.0, 88.0, -88.0, -87.5, 104.0, -104.0, -20.0], device="cuda").to(dt)
+    eye = torch.eye(width(N, a), device="cuda").to(dt)
+    out, pre = torch.zeros((T, N), dtype=dt, device="cuda"), torch.zeros_like(x)
+    B.ep_linear(x, eye, out, dtype, act=ACTS[a], preact=pre)
+    assert torch.equal(pre, x)             # one product is not rounded
+    z = x.double()
+    tiny = 2.0 ** -80 * (1 + (z[:, N:].abs() if a == "swiglu" else 0))
+    check(out, act(z, a), act_error(z, 0 * z, a) + tiny, "out")
+    d = randn((T, N), dt, g)
+    dz = torch.zeros_like(x)
+    B.ep_act_grad(d, x, dz, dtype, ACTS[a])
+    tiny = 2.0 ** -80 * (1 + z.abs().amax()) * d.double().abs().amax()
+    check(dz, act_grad(d.double(), z, a), act_grad_error(d.double(), 0 * d.double(), z, a) + tiny, "dz")
