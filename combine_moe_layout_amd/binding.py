@@ -451,14 +451,14 @@ class _Call:
         return p
 
     def output(self, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
-               may_be: int | None = None) -> int | None:
+               may_be: tuple = ()) -> int | None:
         """The same for an output, which must not share memory with a tensor taken before it
-        (but may be the one at address may_be)."""
+        (but may be one of those named in may_be, from its first element on)."""
         p = self.operand(t, name, dtype, shape)
         if p is not None:
             mine = self.ranges[-1]
             for lo, hi, other in self.ranges[:-1]:
-                if lo < mine[1] and p < hi and not (lo == p == may_be):
+                if lo < mine[1] and p < hi and not (lo == p and other in may_be):
                     raise ValueError("%s overlaps %s" % (name, other))
         return p
 
@@ -544,7 +544,7 @@ def ep_linear(x: torch.Tensor, weights: torch.Tensor, out: torch.Tensor, dtype: 
     res = c.operand(residual, "residual", et, (T, N))
     c.run("ep_linear", stream, c.operand(x, "x", et, (T, K)), c.operand(weights, "weights", et, (W, K)),
           c.operand(bias, "bias", et, (W,)), res, T, K, N, dtype, act,
-          c.output(preact, "preact", et, (T, W)), c.output(out, "out", et, (T, N), may_be=res))
+          c.output(preact, "preact", et, (T, W)), c.output(out, "out", et, (T, N), may_be=("residual",)))
 
 
 def ep_linear_grad_x(dy: torch.Tensor, weights: torch.Tensor, dx: torch.Tensor, dtype: int,
@@ -577,9 +577,9 @@ def ep_act_grad(dy: torch.Tensor, preact: torch.Tensor, dz: torch.Tensor, dtype:
     T, n, et = dy.shape[0], dy.shape[1], _elem(dtype)
     shape = (T, _width(n, act))
     d, z = c.operand(dy, "dy", et, (T, n)), c.operand(preact, "preact", et, shape)
-    same = dz.data_ptr()                   # element by element: dz may be either input
+    # element by element: dz may be an input of its own width
     c.run("ep_act_grad", stream, d, z, T, n, dtype, act,
-          c.output(dz, "dz", et, shape, may_be=same if act != EP_ACT_SWIGLU or same == z else None))
+          c.output(dz, "dz", et, shape, may_be=("preact",) if act == EP_ACT_SWIGLU else ("dy", "preact")))
 
 
 def ep_combine_grad(dout: torch.Tensor, expert_out: torch.Tensor | None, topk_weights: torch.Tensor,

@@ -134,11 +134,10 @@ __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
 }
 
 // dz = dy act'(z), 8 columns to a lane; swiglu: z and dz rows are 2n wide.
+// (dz may be dy or z: no __restrict__.)
 template <bool kF16>
-__global__ __launch_bounds__(256) void act_grad_kernel(const u32x4* __restrict__ dy,
-                                                       const u32x4* __restrict__ z, int64_t vecs,
-                                                       int32_t row_vecs, int32_t act,
-                                                       u32x4* __restrict__ dz) {
+__global__ __launch_bounds__(256) void act_grad_kernel(const u32x4* dy, const u32x4* z, int64_t vecs,
+                                                       int32_t row_vecs, int32_t act, u32x4* dz) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * 256) {
     float d[8], a[8];
     unpack8<kF16>(dy[i], d);

@@ -127,7 +127,7 @@ def test_binding_refuses_wrong_tensors():
     """Shapes, types, strides, overlaps and layouts that do not fit, before anything is enqueued."""
     lay_ = B.EpLayout(4, 2, 3, 1)
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
-    x, w, out = z(8, 16), z(3, 24, 16), z(8, 24)
+    x, w, out, wide = z(8, 16), z(3, 24, 16), z(8, 24), z(8, 16)
     cases = [lambda: B.ep_expert_gemm(x, w[:2].contiguous(), lay_, out, 0),
              lambda: B.ep_expert_gemm(z(7, 16), w, lay_, out, 0),
              lambda: B.ep_expert_gemm(x.half(), w, lay_, out, 0),
@@ -144,6 +144,9 @@ def test_binding_refuses_wrong_tensors():
              lambda: B.ep_expert_gemm_grad_w(out, x, lay_, w, 0, dbias=z(3, 16)),
              lambda: B.ep_linear(x, w[0], out, 0, residual=z(8, 16)),
              lambda: B.ep_linear(x, z(16, 16), x, 0),
+             lambda: B.ep_linear(x, z(16, 16), x, 0, residual=x),   # may be the residual, not x too
+             lambda: B.ep_act_grad(wide[:4], z(8, 32)[:4], wide[:4].view(2, 32), 0, B.EP_ACT_SWIGLU),
+             lambda: B.ep_act_grad(wide[:4], wide.view(4, 32), wide.view(4, 32), 0, B.EP_ACT_SWIGLU),
              lambda: B.ep_linear_grad_w(out, z(7, 16), w[0], 0),
              lambda: B.ep_act_grad(x, x, out, 0, B.EP_ACT_SILU),
              lambda: B.ep_combine_grad(z(4, 16), x, z(4, 2), lay_, z(8, 16), None, 0),
