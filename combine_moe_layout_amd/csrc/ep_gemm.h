@@ -252,13 +252,27 @@ __device__ __forceinline__ float silu_slope(float z) {
   const float p = sigmoid<kExact>(z);
   return p * (1.0f + z * (1.0f - p));
 }
-__device__ __forceinline__ float normal_cdf(float z) {
-  return 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+// The normal distribution's Phi(z), and exp(-z^2 / 2) of its density, by Abramowitz
+// and Stegun's 7.1.26: erfc(x) = t (a1 + t (a2 + ..)) exp(-x^2), t = 1 / (1 + p x),
+// x = |z| / sqrt(2), off by at most 1.5e-7.  One exponential serves both, and the
+// lower tail is not a difference of nearly equal numbers.  (With erff and expf the rows of the
+// gelu gradients of 1803 rows, 24 experts, 392 x 520 take 20 us instead of 16.)
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+  bell = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+  const float a = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                       0.254829592f);
+  const float tail = 0.5f * t * a * bell;
+  return z < 0.0f ? tail : 1.0f - tail;
 }
 __device__ __forceinline__ float act_value(int32_t act, float z) {
   switch (act) {
     case EP_ACT_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    case EP_ACT_GELU: return z * normal_cdf(z);
+    case EP_ACT_GELU: {
+      float bell;
+      return z * normal_cdf(z, bell);
+    }
     case EP_ACT_SILU: return silu(z);
     default: return z;
   }
@@ -268,8 +282,11 @@ template <bool kExact = false>
 __device__ __forceinline__ float act_backward(int32_t act, float d, float z) {
   switch (act) {
     case EP_ACT_RELU: return z > 0.0f ? d : 0.0f;
-    case EP_ACT_GELU:
-      return d * (normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z));
+    case EP_ACT_GELU: {
+      float bell;
+      const float cdf = normal_cdf(z, bell);
+      return d * (cdf + z * 0.39894228040143268f * bell);
+    }
     case EP_ACT_SILU: return d * silu_slope<kExact>(z);
     default: return d;
   }
