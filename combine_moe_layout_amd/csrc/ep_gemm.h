@@ -463,8 +463,8 @@ struct TileStore {
 
 // Picks the kernel for a 16-bit product.
 hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream);
-// Forward only; rows: about how many each group has.
-hipError_t launch_gemm_few(const GemmArgs& g, int64_t rows, bool wide, bool f16, hipStream_t stream);
+// rows: about how many each group has.  wide: 64 x 64 tiles (the gradients' always are).
+hipError_t launch_gemm_few(const GemmArgs& g, int mode, int64_t rows, bool wide, bool f16, hipStream_t stream);
 hipError_t launch_gemm_fp8(const GemmArgs& g, bool mx, hipStream_t stream);
 // launch_gemm_tile: `mode` 0 forward, 1 rows' gradient, 2 weights' gradient.
 hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, hipStream_t stream);

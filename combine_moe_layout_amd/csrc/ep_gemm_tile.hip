@@ -503,12 +503,23 @@ hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, h
 //   reduction 7168: 16 rows, 4096 columns    13 /  31 /  89
 //                   64 rows, 4096 columns    22 /  33 /  91
 //                   256 rows, 4096 columns      /  40 /  72 (256 tiles of 64 x 64)
-//                   512 rows, 4096 columns      /  77 /  73
+//                   512 rows, 4096 columns      /  77 /  65
 //   reduction 4096: 16 rows, 16,384 columns  28 /  24 /
 //                   64 rows, 16,384 columns  50 /  27 /  39
 //   reduction 2048: 1024 rows, 1024 columns     /  15 /  25 (256)
-//                   2048 rows, 1024 columns     /  28 /  26
+//                   2048 rows, 1024 columns     /  28 /  24
 //   reduction 2048, 32 experts of 1024 columns: 16 rows each (512) 41 / 29 / 24
+// The gradients, 64 x 64 / 128 x 128:
+//   rows', 16,384 x 4096, 16 rows            72 / 130 (64)
+//          4096 x 7168, 128 rows             27 /  42 (224)
+//          4096 x 7168, 256 rows             49 /  42 (448)
+//          128 x 7168, 16 rows              5.7 / 5.1 (a reduction of 128)
+//   weights', 9689 rows, 184 x 840           61 /  99 (42)
+//             4096 rows, 1024 x 1024         31 /  46 (256)
+//             8192 rows, 1024 x 2048        101 /  86 (512)
+//             256 rows, 512 x 512           7.2 / 7.1 (64)
+//             16 rows, 1024 x 1024          7.6 / 5.5 (256)
+// so for them only from a reduction of 256 on.
 // Otherwise 256 x 256 tiles where the groups have the rows for them and there
 // are enough tiles for every CU.
 hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream) {
@@ -517,9 +528,10 @@ hipError_t launch_gemm(const GemmArgs& g, int mode, bool f16, hipStream_t stream
   const int64_t groups = mode == kWeightsGrad || r.wanted > r.E ? r.E : r.wanted;
   const int64_t columns = (int64_t)g.out_cols * (mode == kForward && g.act == EP_ACT_SWIGLU ? 2 : 1);
   if (mode == kForward && rows <= 64 && groups * ((columns + 127) / 128) * ((rows + 15) / 16) <= 128)
-    return launch_gemm_few(g, rows, false, f16, stream);
-  if (mode == kForward && groups * ((rows + 63) / 64) * ((columns + 63) / 64) <= kChipCUs)
-    return launch_gemm_few(g, rows, true, f16, stream);
+    return launch_gemm_few(g, mode, rows, false, f16, stream);
+  const int64_t reduce = mode == kWeightsGrad ? (r.wanted + r.E - 1) / r.E : g.reduce;
+  if (groups * ((rows + 63) / 64) * ((columns + 63) / 64) <= kChipCUs && (mode == kForward || reduce >= 256))
+    return launch_gemm_few(g, mode, rows, true, f16, stream);
   const int64_t tiles = groups * ((rows + 255) / 256) * ((columns + 255) / 256);
   return launch_gemm_tile(g, mode, f16, rows >= 192 && tiles >= kChipCUs, stream);
 }

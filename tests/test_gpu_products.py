@@ -104,9 +104,10 @@ def test_expert_gemm_large_groups(name, T, K, N):
 
 
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
-@pytest.mark.parametrize("T,k,E,cap,D,F", [(1500, 2, 6, 0, 136, 5440), (900, 2, 4, 500, 264, 8200)])
-def test_expert_products_in_large_tiles(name, T, k, E, cap, D, F):
-    """256 tiles of 256 x 256 and more, of every kind: up with a bias, its gradients by rows and by
+@pytest.mark.parametrize("T,k,E,cap,D,F", [(1500, 2, 6, 0, 136, 5440), (900, 2, 4, 500, 312, 72),
+                                           (2000, 1, 5, 0, 264, 136), (900, 2, 4, 500, 264, 8200)])
+def test_expert_products_in_tiles_of_every_size(name, T, k, E, cap, D, F):
+    """256 tiles of 256 x 256 and more, or a few of 64 x 64, of every kind: up with a bias, its gradients by rows and by
     weights (adding to what was there, and in the operands' type)."""
     note("large tiles", name, T, k, E, cap, D, F)
     dtype, dt = TYPES[name]
@@ -390,7 +391,9 @@ def test_linear(name, a, T, K, N):
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 @pytest.mark.parametrize("a", list(ACTS))
 @pytest.mark.parametrize("T,K,N", [(1, 64, 64), (5, 24, 1032), (17, 264, 520), (300, 520, 256), (0, 64, 72),
-                                     (2100, 7240, 200), (200, 7240, 2104)])
+                                     (2100, 7240, 200), (200, 7240, 2104),
+                                     # waves that share the reduction; none left over in the last chunk
+                                     (70, 392, 1160), (1100, 72, 136), (65, 1000, 256), (256, 64, 72)])
 def test_linear_gradients(name, a, T, K, N):
     note("linear grads", name, a, T, K, N)
     dtype, dt = TYPES[name]
