@@ -255,8 +255,9 @@ __device__ __forceinline__ float silu_slope(float z) {
 // The normal distribution's Phi(z), and exp(-z^2 / 2) of its density, by Abramowitz
 // and Stegun's 7.1.26: erfc(x) = t (a1 + t (a2 + ..)) exp(-x^2), t = 1 / (1 + p x),
 // x = |z| / sqrt(2), off by at most 1.5e-7.  One exponential serves both, and the
-// lower tail is not a difference of nearly equal numbers.  (With erff and expf the rows of the
-// gelu gradients of 1803 rows, 24 experts, 392 x 520 take 20 us instead of 16.)
+// lower tail is not a difference of nearly equal numbers.  (With erff and expf the
+// rows' gradient through gelu of 1803 rows, 24 experts, 392 x 520 takes 20 us
+// instead of 16.)
 __device__ __forceinline__ float normal_cdf(float z, float& bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
@@ -307,8 +308,8 @@ struct TileStore {
   // A wave hands its results to itself through its quarter of the ring, so that
   // a lane gets 8 neighbouring columns of a row, neighbouring lanes the next
   // ones, and every store covers whole cache lines.  16-byte chunk c of row r
-  // lies at c ^ (r & 15) (as far as the row has chunks): the 16 rows that one store instruction writes at the
-  // same column touch every bank once.
+  // lies at c ^ (r & 15) (as far as the row has chunks): the 16 rows that one
+  // store instruction writes at the same column touch every bank once.
   static constexpr int kFit = kWaveBytes / (16 * kWaveCols * 4);  // blocks of rows that fit at once
   static constexpr int pass_blocks() {  // the largest part of TM that fits
     int n = kFit < TM ? kFit : TM;

@@ -10,14 +10,13 @@
 // swiglu half of them gates and half the ups of the same columns) and 16 TM rows,
 // and its waves share out the reduction in chunks of 64.  TN = 1: a product of
 // 4096 columns has a workgroup for every CU; TM = TN = 4 for more rows, and for
-// the gradients.  Each wave has a ring of
-// chunks of both operands in LDS to itself, so there is no barrier before the
-// end, and a workgroup has 8 chunks or more on their way, where tiles whose waves
-// share every chunk have two.  (LDS is for the address unit: a load costs it 2.6
-// cycles for each 128-byte line that it touches.  In the order of the matrix
-// instruction a load touches 16 lines; through LDS it takes 8 whole ones.)  The
-// waves' sums meet in LDS and are added in wave order, so the result does not
-// depend on timing.
+// the gradients.  Each wave has a ring of chunks of both operands in LDS to
+// itself, so there is no barrier before the end, and a workgroup has 8 chunks or
+// more on their way, where tiles whose waves share every chunk have two.  (LDS is
+// for the address unit: a load costs it 2.6 cycles for each 128-byte line that it
+// touches.  In the order of the matrix instruction a load touches 16 lines;
+// through LDS it takes 8 whole ones.)  The waves' sums meet in LDS and are added
+// in wave order, so the result does not depend on timing.
 //
 // Measured, reduction 7168 and 4096 columns: 1 row 11.8 us (58.7 MB, 5.0 TB/s), 16
 // rows 14, 32 rows 17, 64 rows 22; 256 rows 40 us (TN = 4).  Before the rings, with
