@@ -63,7 +63,8 @@ __device__ __forceinline__ float wave_sums(const float (&v)[N], int& index) {
 
 // lanes: threads of one token (a multiple of 64); the block holds blockDim / lanes
 // tokens.  kPairs: pairs of one workgroup, splits: workgroups per token.
-template <bool kF16, bool kDw, int kPairs>
+// kStream: y does not stay in the last-level cache.
+template <bool kF16, bool kDw, bool kStream, int kPairs>
 __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
     const u32x4* __restrict__ dout, const u32x4* __restrict__ y, const float* __restrict__ w,
     const int32_t* __restrict__ slot, int64_t tokens, int32_t k, int32_t vecs, int32_t lanes,
@@ -93,7 +94,11 @@ __global__ __launch_bounds__(kMaxLanes) void combine_grad_kernel(
       u32x4 rows[kPairs];
       if constexpr (kDw) {  // a pair without a row reads row 0, and its sum is dropped
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) rows[j] = load_nt(y + max(row[j], (int64_t)0) * vecs + v);
+        for (int j = 0; j < kPairs; ++j) {
+          const u32x4* const from = y + max(row[j], (int64_t)0) * vecs + v;
+          if constexpr (kStream) rows[j] = load_nt(from);
+          else rows[j] = *from;
+        }
       }
       float d[8];
       unpack8<kF16>(mine, d);
@@ -188,15 +193,21 @@ hipError_t combine_grad(const void* dout, const void* y, const float* w, const e
         static_cast<const u32x4*>(dout), static_cast<const u32x4*>(y), w, L.slot_idx, L.num_tokens,
         L.num_topk, vecs, lanes, splits, static_cast<u32x4*>(dy), dw);
   };
-  const auto sized = [&](auto with_dw) {
-    constexpr bool kDw = decltype(with_dw)::value;
-    if (pairs == 4) args(combine_grad_kernel<kF16, kDw, 4>);
-    else if (pairs == 3) args(combine_grad_kernel<kF16, kDw, 3>);
-    else if (pairs == 2) args(combine_grad_kernel<kF16, kDw, 2>);
-    else args(combine_grad_kernel<kF16, kDw, 1>);
+  const auto sized = [&](auto with_dw, auto streams) {
+    constexpr bool kDw = decltype(with_dw)::value, kStream = decltype(streams)::value;
+    if (pairs == 4) args(combine_grad_kernel<kF16, kDw, kStream, 4>);
+    else if (pairs == 3) args(combine_grad_kernel<kF16, kDw, kStream, 3>);
+    else if (pairs == 2) args(combine_grad_kernel<kF16, kDw, kStream, 2>);
+    else args(combine_grad_kernel<kF16, kDw, kStream, 1>);
   };
-  if (dw != nullptr) sized(std::true_type());
-  else sized(std::false_type());
+  // y is loaded past the caches where y and dy together outgrow the last-level
+  // cache's 256 MiB.  Past against through them, hidden 7168, top-8: 128 tokens 7.9
+  // against 6.1 us, 1024 (112 MiB of y) 54 and 50, 1536 (168 MiB) 78 and 79, 4096
+  // 194 and 210, 8192 387 and 408.
+  const bool stream_y = L.num_tokens * (int64_t)L.num_topk * hidden * 2 > (int64_t)128 << 20;
+  if (dw == nullptr) sized(std::false_type(), std::false_type());  // y is not read
+  else if (stream_y) sized(std::true_type(), std::true_type());
+  else sized(std::true_type(), std::false_type());
   return hipGetLastError();
 }
 

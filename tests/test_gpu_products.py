@@ -483,7 +483,10 @@ def magnitude(i, leaves, dout, a, d):
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 @pytest.mark.parametrize("T,k,E,cap,H,masked", [(1, 1, 2, 0, 8, 0.0), (37, 3, 5, 0, 200, 0.3), (50, 8, 16, 11, 1024, 0.0),
                                                  (300, 2, 4, 0, 8200, 0.0), (130, 9, 12, 0, 64, 0.1),
-                                                 (1100, 4, 8, 0, 512, 0.0), (6, 2, 4, 2, 72, 1.0), (0, 2, 4, 0, 64, 0.0)])
+                                                 (1100, 4, 8, 0, 512, 0.0), (6, 2, 4, 2, 72, 1.0), (0, 2, 4, 0, 64, 0.0),
+                                                 (1000, 5, 8, 0, 72, 0.1),
+                                                 # more than 128 MiB of rows
+                                                 (6000, 3, 6, 0, 4104, 0.1), (2500, 8, 16, 1100, 4096, 0.0)])
 def test_combine_grad(name, T, k, E, cap, H, masked):
     note("combine_grad", name, T, k, E, cap, H)
     dtype, dt = TYPES[name]
