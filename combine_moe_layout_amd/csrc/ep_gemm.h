@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "ep_device.h"
+#include "ep_gemm_index.h"
 #include "ep_internal.h"
 
 namespace ep {

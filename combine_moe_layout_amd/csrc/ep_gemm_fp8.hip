@@ -76,16 +76,8 @@ struct Fp8Gemm {
 
   __device__ __forceinline__ Fp8Gemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
-  // Row of the matrix operand at place p of the tile's LDS rows: for swiglu the
-  // first half of a wave's rows are gates, the second half the ups of the same columns.
-  __device__ __forceinline__ int matrix_row(int p) const {
-    if constexpr (kGlu) {
-      const int w = p / kWaveCols, in = p % kWaveCols, half = kWaveCols / 2;
-      const int n = t.col * kOutCols + w * half + in % half;
-      return min(n, g.out_cols - 1) + (in >= half ? g.out_cols : 0);
-    } else {
-      return min(t.col * kCols + p, g.out_cols - 1);
-    }
+  __device__ __forceinline__ int row_at(int p, int rows = 1) const {
+    return matrix_row(kGlu, p, kWaveCols, t.col * kOutCols, g.out_cols, rows);
   }
 
   __device__ __forceinline__ void setup() {
@@ -106,12 +98,12 @@ struct Fp8Gemm {
       const int row = (wave * kALoads + i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
       a_off[i] = (uint32_t)min(row, t.rows - 1) * (uint32_t)g.lda + chunk * 16;
     }
-    // (a wave's 32 rows of the matrix operand are neighbours in memory too: of 32
-    // rows all exist or none, as the columns are a multiple of 128)
+    // A wave's rows of the matrix operand are neighbours in memory too, and since the
+    // columns are a multiple of 128 all of them have a column or none: a wave of
+    // places past the last column loads the last rows that there are.
     const int row = wave * kBLoads * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-    const int wave_row = matrix_row(wave * kBLoads * 8);
-    b0 += (int64_t)wave_row * g.ldb;
-    b_off[0] = (uint32_t)(matrix_row(row) - wave_row) * (uint32_t)g.ldb + chunk * 16;
+    b0 += (int64_t)row_at(wave * kBLoads * 8, kBLoads * 8) * g.ldb;
+    b_off[0] = (uint32_t)(lane >> 3) * (uint32_t)g.ldb + chunk * 16;
     b_off[1] = b_off[0] ^ 64;
     const int q = lane >> 4, m = lane & 15;
     const uint32_t in_row = m * kStage + ((q ^ ((m >> 1) & 7)) << 4);
@@ -124,7 +116,7 @@ struct Fp8Gemm {
     if (kMx && wave >= 4) {
       s0 = bs0;
       s_step = kScalePitch;
-      s_off = (uint32_t)matrix_row(min(p, kCols - 1)) * (uint32_t)(g.ldb / 32);
+      s_off = (uint32_t)row_at(min(p, kCols - 1)) * (uint32_t)(g.ldb / 32);
     } else {
       s0 = static_cast<const char*>(g.a_scales) + t.row0 * g.a_scale_row * 4;
       s_step = kQuad ? 16 : g.a_scale_step * 4;
@@ -134,8 +126,8 @@ struct Fp8Gemm {
     bs_read = kScalesAt + (256 + wn * kWaveCols + m) * kScalePitch + q;
     // The wave's columns (32 gates and 32 ups, or 64) lie in one block of 128 each.
     const int64_t per_row = g.ldb / 128;
-    block0 = (uint32_t)(matrix_row(wn * kWaveCols) / 128 * per_row);
-    block1 = (uint32_t)(matrix_row(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
+    block0 = (uint32_t)(row_at(wn * kWaveCols) / 128 * per_row);
+    block1 = (uint32_t)(row_at(wn * kWaveCols + kWaveCols / 2) / 128 * per_row);
   }
 
   // Load j of stage s: of the row operand (into slot `slot`), of the matrix

@@ -120,17 +120,8 @@ struct TileGemm {
 
   __device__ __forceinline__ TileGemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
-  // Row of the matrix operand that stands at place p of the tile's LDS rows:
-  // for swiglu the first half of a wave's rows are gates, the second half the
-  // ups of the same columns.
-  __device__ __forceinline__ int matrix_row(int p) const {
-    if constexpr (kGlu && kMode == kForward) {
-      const int w = p / kWaveCols, in = p % kWaveCols, half = kWaveCols / 2;
-      const int n = t.col * kOutCols + w * half + in % half;
-      return min(n, g.out_cols - 1) + (in >= half ? g.out_cols : 0);
-    } else {
-      return min(t.col * kCols + p, g.out_cols - 1);
-    }
+  __device__ __forceinline__ int row_at(int p) const {
+    return matrix_row(kGlu && kMode == kForward, p, kWaveCols, t.col * kOutCols, g.out_cols);
   }
 
   __device__ __forceinline__ void setup() {
@@ -153,12 +144,12 @@ struct TileGemm {
     // A wave's rows of the matrix operand are neighbours in memory (all gates, or
     // all ups): offsets count from their first.
     static_assert(!kBContig || kWaveCols / 2 % (B::kLoads * 8) == 0, "a wave loads gates or ups");
-    const int wave_row = kBContig ? matrix_row(wave * B::kLoads * 8) : 0;
+    const int wave_row = kBContig ? row_at(wave * B::kLoads * 8) : 0;
     if constexpr (kBContig) b0 += (int64_t)wave_row * g.ldb * 2;
 #pragma unroll
     for (int i = 0; i < B::kLoads; ++i) {
       const int row = B::load_row(i), chunk = B::load_chunk(i);
-      if constexpr (kBContig) b_off[i] = (uint32_t)(matrix_row(row) - wave_row) * (uint32_t)g.ldb * 2u + chunk * 16;
+      if constexpr (kBContig) b_off[i] = (uint32_t)(row_at(row) - wave_row) * (uint32_t)g.ldb * 2u + chunk * 16;
       else b_off[i] = (uint32_t)row * (uint32_t)g.ldb * 2u + min(chunk * 8, b_limit - 8) * 2;
     }
     a_step = kAContig ? kUnit * 2 : (int64_t)kUnit * g.lda * 2;
