@@ -110,10 +110,6 @@ struct Tile {
 // skips a tile's blocks of 16 rows that it does not have).
 // Every wave does the search by itself: its lanes hold E/64 groups each.
 constexpr int kXcds = 8;
-// ceil(count / height); a count may be as large as 2^31 - 1.
-__device__ __forceinline__ int32_t tiles_of(int32_t count, int32_t height) {
-  return (int32_t)(((uint32_t)count + (uint32_t)height - 1) / (uint32_t)height);
-}
 __device__ __forceinline__ int64_t uniform(int64_t v) {  // the same in every lane: to scalar registers
   return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(v >> 32)) << 32) |
                    (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)v));

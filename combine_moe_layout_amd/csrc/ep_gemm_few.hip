@@ -131,7 +131,7 @@ __global__ __launch_bounds__(waves_of(TM) * 64, waves_of(TM) / 4) void gemm_few_
       offset[j] = (uint32_t)min(of_b ? r % kOut : r, last) * (uint32_t)ld * 2u + chunk * 16;
     }
   }
-  const int chunks = (reduce + kChunk - 1) / kChunk, whole = reduce / kChunk;
+  const int chunks = tiles_of(reduce, kChunk), whole = reduce / kChunk;
   const auto load = [&](int c, int slot) {
     const uint32_t to = ring + slot * kSlotBytes;
 #pragma unroll

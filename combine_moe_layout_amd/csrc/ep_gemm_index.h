@@ -8,6 +8,12 @@
 
 namespace ep {
 
+// ceil(count / height): row tiles of a group, chunks of a reduction.  A count may be
+// as large as 2^31 - 1.
+constexpr int32_t tiles_of(int32_t count, int32_t height) {
+  return (int32_t)(((uint32_t)count + (uint32_t)height - 1) / (uint32_t)height);
+}
+
 // A tile's LDS holds rows of the matrix operand, `wave_cols` to a column of waves.
 // Row of the matrix at place p of them, or the first of `rows` neighbouring ones
 // from place p on; first_col: the tile's first result column, out_cols: all result

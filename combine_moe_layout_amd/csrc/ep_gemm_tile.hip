@@ -134,7 +134,7 @@ struct TileGemm {
     a_place = lds0 + wave * A::kLoads * 1024;
     b_place = lds0 + kASlots * A::kBytes + wave * B::kLoads * 1024;
     whole_units = reduce / kUnit;
-    units = (reduce + kUnit - 1) / kUnit;
+    units = tiles_of(reduce, kUnit);
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int row = A::load_row(i), chunk = A::load_chunk(i);

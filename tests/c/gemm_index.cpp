@@ -1,9 +1,11 @@
 // gemm_index.cpp -- walks the index arithmetic of the matrix-product kernels
 // (csrc/ep_gemm_index.h) on the host: every row of the matrix operand that a tile
-// loads lies inside its expert's matrix.  (Results do not show a row past it: its
-// products are dropped.)  Exit status 0 if all hold; the first that does not is
-// printed.
+// loads lies inside its expert's matrix (results do not show a row past it: its
+// products are dropped), and counts up to 2^31 - 1 rows come out whole.  Exit status
+// 0 if all hold; the first that does not is printed.
 #include <stdio.h>
+
+#include <initializer_list>
 
 #include "ep_gemm_index.h"
 
@@ -33,9 +35,23 @@ int walk(bool glu, int wave_cols, int out_cols, int rows) {
   return 0;
 }
 
+// Tiles and chunks of a count, up to the largest.
+int count_tiles() {
+  const int64_t last = INT32_MAX;
+  for (int height : {16, 32, 64, 128, 192, 256})
+    for (int64_t n : {(int64_t)0, (int64_t)1, (int64_t)height - 1, (int64_t)height, (int64_t)height + 1,
+                      last - height, last - height + 1, last - height + 2, last - 1, last})
+      if (ep::tiles_of((int32_t)n, height) != (n + height - 1) / height) {
+        printf("%d tiles of %d in %lld rows\n", ep::tiles_of((int32_t)n, height), height, (long long)n);
+        return 1;
+      }
+  return 0;
+}
+
 }  // namespace
 
 int main() {
+  if (count_tiles()) return 1;
   for (int glu = 0; glu < 2; ++glu)
     for (int wave_cols = 32; wave_cols <= 64; wave_cols *= 2) {
       // FP8: a wave of 8 brings half a column of waves' places, counted from the first
