@@ -67,18 +67,8 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // --------------------------------------------------------------------------
-// Ragged groups.  Group e owns rows [first, first + count) of the row operand
-// and matrix e of the other one.  A dense product is one group of R rows.
+// Ragged groups (RowGroups in ep_gemm_index.h).
 // --------------------------------------------------------------------------
-struct RowGroups {
-  const int32_t* first;  // [E + 1] first rows (contiguous layout); NULL: one group of all rows
-  const int32_t* count;  // [E] rows wanted by each group (padded layout); NULL when contiguous
-  int32_t E;
-  int32_t capacity;      // rows per group (padded layout)
-  int64_t rows;          // R
-  int64_t wanted;        // pairs routed: at most this many rows are used
-};
-
 __device__ __forceinline__ int32_t group_count(const RowGroups& g, int32_t e) {
   if (g.first == nullptr) return (int32_t)g.rows;
   if (g.capacity > 0) return min(max(g.count[e], 0), g.capacity);
@@ -162,14 +152,6 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   return t.rows > 0;
 }
 
-// Row tiles that R rows in E groups can make at most.
-inline int64_t max_row_tiles(const RowGroups& g, int32_t height) {
-  if (g.first == nullptr) return (g.rows + height - 1) / height;
-  const int64_t most = g.wanted / height + (g.wanted < g.E ? g.wanted : g.E);
-  if (g.capacity == 0) return most;
-  const int64_t padded = (int64_t)g.E * ((g.capacity + height - 1) / height);
-  return padded < most ? padded : most;
-}
 // A launch holds fewer than 2^32 threads.
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 

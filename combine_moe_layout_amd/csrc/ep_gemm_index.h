@@ -14,6 +14,26 @@ constexpr int32_t tiles_of(int32_t count, int32_t height) {
   return (int32_t)(((uint32_t)count + (uint32_t)height - 1) / (uint32_t)height);
 }
 
+// Ragged groups.  Group e owns rows [first, first + count) of the row operand
+// and matrix e of the other one.  A dense product is one group of R rows.
+struct RowGroups {
+  const int32_t* first;  // [E + 1] first rows (contiguous layout); NULL: one group of all rows
+  const int32_t* count;  // [E] rows wanted by each group (padded layout); NULL when contiguous
+  int32_t E;
+  int32_t capacity;      // rows per group (padded layout)
+  int64_t rows;          // R
+  int64_t wanted;        // pairs routed: at most this many rows are used
+};
+
+// Row tiles that R rows in E groups can make at most.
+inline int64_t max_row_tiles(const RowGroups& g, int32_t height) {
+  if (g.first == nullptr) return (g.rows + height - 1) / height;
+  const int64_t most = g.wanted / height + (g.wanted < g.E ? g.wanted : g.E);
+  if (g.capacity == 0) return most;
+  const int64_t padded = (int64_t)g.E * tiles_of(g.capacity, height);
+  return padded < most ? padded : most;
+}
+
 // A tile's LDS holds rows of the matrix operand, `wave_cols` to a column of waves.
 // Row of the matrix at place p of them, or the first of `rows` neighbouring ones
 // from place p on; first_col: the tile's first result column, out_cols: all result

@@ -1,8 +1,8 @@
 // gemm_index.cpp -- walks the index arithmetic of the matrix-product kernels
 // (csrc/ep_gemm_index.h) on the host: every row of the matrix operand that a tile
 // loads lies inside its expert's matrix (results do not show a row past it: its
-// products are dropped), and counts up to 2^31 - 1 rows come out whole.  Exit status
-// 0 if all hold; the first that does not is printed.
+// products are dropped), and counts up to 2^31 - 1 rows and the grids made of them
+// come out whole.  Exit status 0 if all hold; the first that does not is printed.
 #include <stdio.h>
 
 #include <initializer_list>
@@ -48,10 +48,31 @@ int count_tiles() {
   return 0;
 }
 
+// The grid's bound on row tiles: E groups of `capacity` rows, `wanted` pairs among them.
+int bound_tiles() {
+  const int32_t last = INT32_MAX;
+  for (int32_t E : {1, 2, 3})
+    for (int32_t capacity : {1, 64, last / 4, last - 300, last - 15, last}) {
+      if ((int64_t)E * capacity > last) continue;
+      for (int64_t wanted : {(int64_t)1, (int64_t)1000, (int64_t)last})
+        for (int height : {16, 64, 128, 192, 256}) {
+          const ep::RowGroups g = {&capacity, &capacity, E, capacity, (int64_t)E * capacity, wanted};
+          const int64_t each = ((int64_t)capacity + height - 1) / height, got = ep::max_row_tiles(g, height);
+          const int64_t rows = wanted < g.rows ? wanted : g.rows;
+          if (got < (rows + height - 1) / height || got > E * each) {
+            printf("%lld tiles of %d for %d x %d rows, %lld pairs\n", (long long)got, height, E, capacity,
+                   (long long)wanted);
+            return 1;
+          }
+        }
+    }
+  return 0;
+}
+
 }  // namespace
 
 int main() {
-  if (count_tiles()) return 1;
+  if (count_tiles() || bound_tiles()) return 1;
   for (int glu = 0; glu < 2; ++glu)
     for (int wave_cols = 32; wave_cols <= 64; wave_cols *= 2) {
       // FP8: a wave of 8 brings half a column of waves' places, counted from the first

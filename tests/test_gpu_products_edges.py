@@ -32,3 +32,29 @@ def test_weights_gradient_of_the_most_rows(T):
     check(db, e.sum(0), 200 * SUM * e.abs().sum(0), "dbias")
     del x
     torch.cuda.empty_cache()
+
+
+def test_one_expert_with_the_largest_capacity():
+    """A few rows in a padded buffer of 2^31 - 1: the grid follows the rows wanted, not the capacity."""
+    cap = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 3 * cap * 16 + 2 ** 30:
+        pytest.skip("needs 104 GB")
+    print("[gpu-products-edges] capacity", cap, flush=True)
+    g = gen(2)
+    lay = B.EpLayout(5, 1, 1, 1, cap)
+    B.ep_get_layout(torch.zeros((5, 1), dtype=torch.int64, device="cuda"), lay)
+    x, out = (torch.empty((cap, 8), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[:5] = torch.randn((5, 8), device="cuda", generator=g).to(torch.bfloat16)
+    out[:8] = 7.0
+    w = torch.randn((1, 8, 8), device="cuda", generator=g).to(torch.bfloat16)
+    B.ep_expert_gemm(x, w, lay, out, B.EP_BF16)
+    dx = torch.empty_like(out)
+    dx[:8] = 7.0
+    B.ep_expert_gemm_grad_x(x, w, lay, dx, B.EP_BF16)
+    torch.cuda.synchronize()
+    v, m = x[:5].double(), w[0].double()
+    check(out[:5], v @ m.T, 8 * SUM * (v.abs() @ m.abs().T), "out")
+    check(dx[:5], v @ m, 8 * SUM * (v.abs() @ m.abs()), "dx")
+    assert (out[5:8] == 7).all() and (dx[5:8] == 7).all()
+    del x, out, dx
+    torch.cuda.empty_cache()
