@@ -41,16 +41,16 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ void load16_to_lds(const void* base, uint32_t byte_offset,
                                               uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(byte_offset),
-               "s"(base), "s"(lds));
+               "s"(base), "s"(lds) : "m0");
 }
 __device__ __forceinline__ void load16_to_lds(const void* lane_address, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(lane_address),
-               "s"(lds));
+               "s"(lds) : "m0");
 }
 // The same for 64 x 4 bytes.
 __device__ __forceinline__ void load4_to_lds(const void* base, uint32_t byte_offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(byte_offset),
-               "s"(base), "s"(lds));
+               "s"(base), "s"(lds) : "m0");
 }
 
 // Waits until at most N of this wave's loads are in flight.
