@@ -294,7 +294,7 @@ struct TileStore {
   static constexpr int kMask = 4 * TN < 16 ? 4 * TN - 1 : 15;  // 16-byte chunks of a row that change places
   static constexpr int kOutCols = kWaveCols * WN / (kGlu && kMode == kForward ? 2 : 1);
 
-  // A wave hands its results to itself through its quarter of the ring, so that
+  // A wave hands its results to itself through its share of the ring, so that
   // a lane gets 8 neighbouring columns of a row, neighbouring lanes the next
   // ones, and every store covers whole cache lines.  16-byte chunk c of row r
   // lies at c ^ (r & 15) (as far as the row has chunks): the 16 rows that one

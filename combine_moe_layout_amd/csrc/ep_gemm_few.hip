@@ -156,7 +156,8 @@ __global__ __launch_bounds__(waves_of(TM) * 64, waves_of(TM) / 4) void gemm_few_
   F ones;
 #pragma unroll
   for (int k = 0; k < 8; ++k) ones[k] = 1;
-  // Chunks wave, wave + kWaves, ..: all but one of the ring's slots ahead.
+  // Chunks wave, wave + kWaves, ..: every slot of the ring is filled, and a slot is
+  // filled again as soon as its chunk has been read.
 #pragma unroll
   for (int i = 0; i < kSlots; ++i)
     if (wave + i * kWaves < chunks) load(wave + i * kWaves, i);

@@ -434,7 +434,7 @@ struct TileGemm {
 };
 
 template <int kMode, bool kF16, bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, TM * TN >= 64 ? 1 : 2) void gemm_tile_kernel(GemmArgs g) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void gemm_tile_kernel(GemmArgs g) {
   typedef TileGemm<kMode, kF16, kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
@@ -500,6 +500,12 @@ hipError_t launch_gemm_tile(const GemmArgs& g, int mode, bool f16, bool large, h
 //   reduction 2048: 1024 rows, 1024 columns     /  15 /  25 (256)
 //                   2048 rows, 1024 columns     /  28 /  24
 //   reduction 2048, 32 experts of 1024 columns: 16 rows each (512) 41 / 29 / 24
+//   reduction 256:  16 rows, 4096 columns   4.0 / 5.6 / 5.7
+//                   64 rows, 2048 columns   4.3 / 7.1 / 6.3
+//                   8 experts of 1024 columns, 32 rows each  8.8 / 5.8 / 6.6
+//   reduction 2048, the same                                16.3 /12.7 /21.0
+// (the last two are where counting 128 x 128 tiles errs: 512 or more workgroups of 16
+// columns, one to a CU for their LDS, go in rounds).
 // The gradients, 64 x 64 / 128 x 128:
 //   rows', 16,384 x 4096, 16 rows            72 / 130 (64)
 //          4096 x 7168, 128 rows             27 /  42 (224)
