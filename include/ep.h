@@ -464,9 +464,9 @@ int ep_expert_gemm_grad_w(const void* dy, const void* x, const ep_layout_t* layo
  * x [rows, in_features], weights [W, in_features], bias [W] or NULL, residual
  * and out [rows, out_features] (residual may be NULL), preact [rows, W] or NULL;
  * W and act as in ep_expert_gemm.  dtype EP_BF16 or EP_F16.  out may be the
- * residual itself.  0 <= rows < 2^31.  Status codes as ep_expert_gemm.  (Any of
- * these products starts up to two threads for every row and 256 product columns;
- * 2^32 of them or more are EP_ERR_LAUNCH.)
+ * residual itself.  0 <= rows < 2^31.  Status codes as ep_expert_gemm.  (A product
+ * of very many rows starts two threads for every row and 256 product columns, an
+ * FP8 one up to three; 2^32 threads or more are EP_ERR_LAUNCH.)
  */
 int ep_linear(const void* x, const void* weights, const void* bias, const void* residual,
               int64_t rows, int32_t in_features, int32_t out_features, int32_t dtype, int32_t act,
