@@ -1,10 +1,10 @@
 """gelu and its slope relative to their values, down to where they leave the type's normal range.
 
 Phi(-|z|) is computed as exp(-z^2 / 2) times a function of |z|, in fp32.  Relative errors for |z|
-up to 13: the function's fit 3.8e-7; its quotient, eight multiply-adds and two products, each half a
-step (2^-24) and the quotient a whole one with at most twice the weight, 13 * 2^-24 = 7.7e-7; 2^x a
+up to 13: the function's fit 5.6e-8; its quotient, nine multiply-adds and two products, each half a
+step (2^-24) and the quotient a whole one with at most twice the weight, 15 * 2^-24 = 8.9e-7; 2^x a
 step, 1.2e-7; the argument z^2 log2(e) / 2 <= 122 is off by its constant's and its product's half
-steps (z^2 of a 16-bit z is exact), 122 * ln 2 * 2 * 2^-24 = 1.01e-5.  Together 1.14e-5, below
+steps (z^2 of a 16-bit z is exact), 122 * ln 2 * 2 * 2^-24 = 1.01e-5.  Together 1.12e-5, below
 2^-16 = 1.53e-5.  The slope Phi(z) + z phi(z) adds two terms that are each that close, and rounds
 once more: 2^-16 of the sum of their magnitudes."""
 import math
