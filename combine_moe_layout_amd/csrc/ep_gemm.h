@@ -231,43 +231,52 @@ __device__ __forceinline__ float silu_slope(float z) {
   const float p = sigmoid<kExact>(z);
   return p * (1.0f + z * (1.0f - p));
 }
-// The normal distribution's Phi(z), and bell = exp(-z^2 / 2) of its density.  The lower
-// tail keeps its digits all the way down:
-//   Phi(-|z|) = bell t R(t),  t = 1 / (1 + q |z|),
-// R of degree 8, fitted here to the least largest relative error, 5.6e-8, over all z
-// (t R(t) runs from 1/2 at z = 0 to 1 / (|z| sqrt(2 pi)) far out, which is q times R's
-// value at t = 0).  In fp32 the tail is off by 1e-6 of itself up to |z| = 3 and by 2^-17
-// at 13, where the exponential's argument is rounded at 122 and a bf16 leaves its normal
-// range.  (1 + erf in fp32 is 0 at z = -6, and a fit of least absolute error, 1.5e-7, is
-// off by 1% at -8.)  One exponential serves both results.  With the library's functions:
-// the activation's own gradient, 8192 x 4096, 64 us by erfcf and expf, 47 by a true
-// quotient and expf, 40 so, which is HBM's time; the rows' gradient through gelu of 1803
-// rows, 24 experts, 392 x 520, 20 us by erff and expf, 16 so.
+// The lower tail of the normal distribution, without its exponential: h(a) of
+//   Phi(-a) = bell h(a),  bell = exp(-a^2 / 2),  a = |z|,
+// so that the tail keeps its digits all the way down.  h = t R(t), t = 1 / (1 + a / 4),
+// R of degree 9, fitted here to the least largest relative error, 3e-9, over all a (h
+// runs from 1/2 at 0 to 1 / (a sqrt(2 pi)) far out, which is R's value at t = 0 over
+// a / 4).  In fp32 the tail is off by 1e-6 of itself up to a = 3 and by 2^-17 at 13,
+// where the exponential's argument is rounded at 122 and a bf16 leaves its normal range.
+// (1 + erf in fp32 is 0 at z = -6, and a fit of least absolute error, 1.5e-7, is off by
+// 1% at -8.)  One exponential serves value and slope.  With the library's functions: the
+// activation's own gradient, 8192 x 4096, 64 us by erfcf and expf, 47 by a true quotient
+// and expf, 40 so, which is HBM's time; the rows' gradient through gelu of 1803 rows, 24
+// experts, 392 x 520, 20 us by erff and expf, 16 so.
 // kExact: the hardware's reciprocal improved by one step, where there is time for it.
 template <bool kExact = false>
-__device__ __forceinline__ float normal_cdf(float z, float& bell) {
-  const float d = fmaf(0.276747495f, fabsf(z), 1.0f);
+__device__ __forceinline__ float normal_tail(float a, float& bell) {
+  const float d = fmaf(0.25f, a, 1.0f);
   float t = __builtin_amdgcn_rcpf(d);
   if constexpr (kExact) t = fmaf(fmaf(-d, t, 1.0f), t, t);
-  bell = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-  float r = fmaf(t, 0.0263261981f, -0.104515716f);
-  r = fmaf(t, r, 0.116044298f);
-  r = fmaf(t, r, -0.0237109531f);
-  r = fmaf(t, r, 0.0816534534f);
-  r = fmaf(t, r, 0.0810042173f);
-  r = fmaf(t, r, 0.102412388f);
-  r = fmaf(t, r, 0.110379197f);
-  r = fmaf(t, r, 0.110406891f);
-  const float tail = t * r * bell;
-  return z < 0.0f ? tail : 1.0f - tail;
+  bell = __builtin_amdgcn_exp2f(a * a * -0.72134752044448170f);
+  float r = fmaf(t, 0.0209641105f, -0.0862399986f);
+  r = fmaf(t, r, 0.105812593f);
+  r = fmaf(t, r, -0.0423424627f);
+  r = fmaf(t, r, 0.0702728241f);
+  r = fmaf(t, r, 0.0565008422f);
+  r = fmaf(t, r, 0.0821602460f);
+  r = fmaf(t, r, 0.0933954401f);
+  r = fmaf(t, r, 0.0997409440f);
+  r = fmaf(t, r, 0.0997354605f);
+  return t * r;
+}
+__device__ __forceinline__ float gelu(float z) {
+  float bell;
+  const float h = normal_tail(fabsf(z), bell);
+  return z * (z < 0.0f ? bell * h : fmaf(-bell, h, 1.0f));
+}
+// Phi(z) + z phi(z) = g bell for z < 0 and 1 - g bell for z >= 0, g = h(a) - a / sqrt(2 pi).
+template <bool kExact = false>
+__device__ __forceinline__ float gelu_slope(float z) {
+  float bell;
+  const float a = fabsf(z), h = normal_tail<kExact>(a, bell), g = fmaf(a, -0.39894228040143268f, h);
+  return z < 0.0f ? bell * g : fmaf(-bell, g, 1.0f);
 }
 __device__ __forceinline__ float act_value(int32_t act, float z) {
   switch (act) {
     case EP_ACT_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    case EP_ACT_GELU: {
-      float bell;
-      return z * normal_cdf(z, bell);
-    }
+    case EP_ACT_GELU: return gelu(z);
     case EP_ACT_SILU: return silu(z);
     default: return z;
   }
@@ -277,11 +286,7 @@ template <bool kExact = false>
 __device__ __forceinline__ float act_backward(int32_t act, float d, float z) {
   switch (act) {
     case EP_ACT_RELU: return z > 0.0f ? d : 0.0f;
-    case EP_ACT_GELU: {
-      float bell;
-      const float cdf = normal_cdf<kExact>(z, bell);
-      return d * (cdf + z * 0.39894228040143268f * bell);
-    }
+    case EP_ACT_GELU: return d * gelu_slope<kExact>(z);
     case EP_ACT_SILU: return d * silu_slope<kExact>(z);
     default: return d;
   }

@@ -1,11 +1,11 @@
 """gelu and its slope relative to their values, down to where they leave the type's normal range.
 
 Phi(-|z|) is computed as exp(-z^2 / 2) times a function of |z|, in fp32.  Relative errors for |z|
-up to 13: the function's fit 5.6e-8; its quotient, nine multiply-adds and two products, each half a
-step (2^-24) and the quotient a whole one with at most twice the weight, 15 * 2^-24 = 8.9e-7; 2^x a
-step, 1.2e-7; the argument z^2 log2(e) / 2 <= 122 is off by its constant's and its product's half
-steps (z^2 of a 16-bit z is exact), 122 * ln 2 * 2 * 2^-24 = 1.01e-5.  Together 1.12e-5, below
-2^-16 = 1.53e-5.  The slope Phi(z) + z phi(z) adds two terms that are each that close, and rounds
+up to 13: the function's fit 3e-9; eleven multiply-adds and two products, each half a step (2^-24),
+and a quotient, a whole one with at most twice the weight, 17 * 2^-24 = 1.01e-6; 2^x a step, 1.2e-7;
+the argument z^2 log2(e) / 2 <= 122 is off by its constant's and its product's half steps (z^2 of a
+16-bit z is exact), 122 * ln 2 * 2 * 2^-24 = 1.01e-5.  Together 1.13e-5, below 2^-16 = 1.53e-5.
+The slope Phi(z) + z phi(z) adds two terms that are each that close, and rounds
 once more: 2^-16 of the sum of their magnitudes."""
 import math
 
@@ -41,7 +41,7 @@ def close(got, ref, before, what):
 @pytest.mark.parametrize("times", [1, 40, 600])
 def test_gelu_of_every_value(name, times):
     """Through a product with the identity, which is exact (rows for each of the kernels)."""
-    print("[gpu-gelu] forward", name, times, flush=True)
+    print("[gpu-activations] forward", name, times, flush=True)
     dtype, dt = TYPES[name]
     x = every_value(dt, -13.0, 13.0).repeat(times, 1)
     eye = torch.eye(64, device="cuda").to(dt)
@@ -57,7 +57,7 @@ def test_gelu_of_every_value(name, times):
 @pytest.mark.parametrize("times", [0, 1, 40, 600])
 def test_gelu_slope_of_every_value(name, times):
     """ep_act_grad (times 0), and the rows' gradient of a product with the identity."""
-    print("[gpu-gelu] slope", name, times, flush=True)
+    print("[gpu-activations] slope", name, times, flush=True)
     dtype, dt = TYPES[name]
     z16 = every_value(dt, -13.0, 13.0).repeat(max(times, 1), 1)
     d = torch.ones_like(z16)
@@ -77,7 +77,7 @@ def test_gelu_slope_of_every_value(name, times):
 @pytest.mark.parametrize("name", ["bf16", "fp16"])
 def test_gelu_with_more_columns_than_rows(name):
     """The kernel for few rows: values along the columns, from the bias alone."""
-    print("[gpu-gelu] few rows", name, flush=True)
+    print("[gpu-activations] few rows", name, flush=True)
     dtype, dt = TYPES[name]
     bias = every_value(dt, -13.0, 13.0).reshape(-1)
     N = bias.numel()
