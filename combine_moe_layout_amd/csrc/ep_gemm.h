@@ -224,13 +224,22 @@ __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (kExact) return 1.0f / (1.0f + expf(-z));
   else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
-template <bool kExact = false>
-__device__ __forceinline__ float silu(float z) { return z * sigmoid<kExact>(z); }
-template <bool kExact = false>
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 __device__ __forceinline__ float silu_slope(float z) {
-  const float p = sigmoid<kExact>(z);
+  const float p = sigmoid(z);
   return p * (1.0f + z * (1.0f - p));
 }
+// d silu'(z) where there is time for it, rounded operation by operation as the formula
+// stands: the gradient that an activation hands on in 16 bits is the one that the same
+// formula gives in fp32 outside of a kernel.  (With multiply-adds a few of 10,000 fp16
+// results went to the other neighbour, and the fp32 weights' gradient of 777 x 1000 x 504
+// made of them was up to 2.8e-5 of its norm away.)
+__device__ __forceinline__ float silu_backward_exact(float d, float z) {
+#pragma clang fp contract(off)
+  const float p = sigmoid<true>(z), q = z * (1.0f - p);
+  return d * p * (1.0f + q);
+}
+
 // The lower tail of the normal distribution, without its exponential: h(a) of
 //   Phi(-a) = bell h(a),  bell = exp(-a^2 / 2),  a = |z|,
 // so that the tail keeps its digits all the way down.  h = t R(t), t = 1 / (1 + a / 4),
@@ -287,7 +296,9 @@ __device__ __forceinline__ float act_backward(int32_t act, float d, float z) {
   switch (act) {
     case EP_ACT_RELU: return z > 0.0f ? d : 0.0f;
     case EP_ACT_GELU: return d * gelu_slope<kExact>(z);
-    case EP_ACT_SILU: return d * silu_slope<kExact>(z);
+    case EP_ACT_SILU:
+      if constexpr (kExact) return silu_backward_exact(d, z);
+      else return d * silu_slope(z);
     default: return d;
   }
 }

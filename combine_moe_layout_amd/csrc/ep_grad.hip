@@ -158,8 +158,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const u32x4* dy, const u3
       unpack8<kF16>(z[at + row_vecs], up);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        du[k] = d[k] * silu<true>(a[k]);
-        d[k] = d[k] * up[k] * silu_slope<true>(a[k]);
+        du[k] = d[k] * a[k] * sigmoid<true>(a[k]);
+        d[k] = silu_backward_exact(d[k] * up[k], a[k]);
       }
       dz[at] = pack8_rne<kF16>(d);
       dz[at + row_vecs] = pack8_rne<kF16>(du);

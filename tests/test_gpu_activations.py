@@ -1,4 +1,5 @@
-"""gelu and its slope relative to their values, down to where they leave the type's normal range.
+"""gelu and its slope relative to their values, down to where they leave the type's normal range, and
+how silu's own gradient is rounded.
 
 Phi(-|z|) is computed as exp(-z^2 / 2) times a function of |z|, in fp32.  Relative errors for |z|
 up to 13: the function's fit 3e-9; eleven multiply-adds and two products, each half a step (2^-24),
@@ -88,3 +89,18 @@ def test_gelu_with_more_columns_than_rows(name):
     ref = z * parts(z)[0]
     for r in range(3):
         close(out[r], ref, REL * ref.abs(), "row %d" % r)
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_silu_gradient_rounds_as_its_formula(name):
+    """ep_act_grad through silu gives the bits of the formula in fp32 operations, each rounded."""
+    print("[gpu-activations] silu", name, flush=True)
+    dtype, dt = TYPES[name]
+    z = every_value(dt, -60.0, 60.0).repeat(8, 1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    d = torch.randn(z.shape, device="cuda", generator=g).to(dt)
+    dz = torch.full_like(z, 7.0)
+    B.ep_act_grad(d, z, dz, dtype, B.EP_ACT_SILU)
+    p = 1 / (1 + torch.exp(-z.float()))
+    assert torch.equal(dz, (d.float() * p * (1 + z.float() * (1 - p))).to(dt))
