@@ -128,6 +128,12 @@ def _demangle(names: list) -> list:
     return names
 
 
+def kernel_label(demangled: str) -> str:
+    """A kernel's name and template arguments, without namespaces, return type and parameters."""
+    n = demangled.replace("(anonymous namespace)::", "").replace("ep::", "").split("(")[0]
+    return n[5:] if n.startswith("void ") else n
+
+
 if __name__ == "__main__":
     if "--resources" in sys.argv:
         rows = resource_usage()
@@ -135,9 +141,8 @@ if __name__ == "__main__":
         print("| kernel | source | VGPR | AGPR | SGPR | LDS B | scratch B/lane | waves/SIMD | spills |")
         print("|---|---|---:|---:|---:|---:|---:|---:|---:|")
         for r, n in zip(rows, names):
-            n = n.replace("ep::", "").split("(")[0]
             print("| `%s` | %s | %d | %d | %d | %d | %d | %d | %d |" % (
-                n, r["source"], r.get("vgpr", -1), r.get("agpr", -1), r.get("sgpr", -1), r.get("lds", -1),
+                kernel_label(n), r["source"], r.get("vgpr", -1), r.get("agpr", -1), r.get("sgpr", -1), r.get("lds", -1),
                 r.get("scratch", -1), r.get("occupancy", -1), r.get("vgpr_spill", 0) + r.get("sgpr_spill", 0)))
     else:
         print(build_library(verbose="-v" in sys.argv))

@@ -1,5 +1,5 @@
-"""Index arithmetic of the matrix products, compiled for the host and walked over sizes on the CPU, and
-what their inline assembly declares."""
+"""Index arithmetic of the matrix products, compiled for the host and walked over sizes on the CPU; what
+their inline assembly declares; how the resource table names them."""
 import os
 import re
 import subprocess
@@ -26,3 +26,10 @@ def test_inline_assembly_names_the_m0_it_writes():
                 seen += 1
                 assert re.search(r':\s*"m0"\s*$', text), (name, text)
     assert seen >= 3
+
+
+def test_resource_table_names_kernels():
+    from combine_moe_layout_amd.build import kernel_label
+    assert kernel_label("void ep::(anonymous namespace)::gemm_few_kernel<0, false, true, 2, 1>(ep::GemmArgs)") == \
+        "gemm_few_kernel<0, false, true, 2, 1>"
+    assert kernel_label("ep::layout_count_kernel(long const*, int)") == "layout_count_kernel"
