@@ -231,7 +231,7 @@ __device__ __forceinline__ float silu_slope(float z) {
 }
 // d silu'(z) where there is time for it, rounded operation by operation as the formula
 // stands: the gradient that an activation hands on in 16 bits is the one that the same
-// formula gives in fp32 outside of a kernel.  (With multiply-adds a few of 10,000 fp16
+// formula gives in fp32 outside of a kernel.  (With multiply-adds one of 9000 fp16
 // results went to the other neighbour, and the fp32 weights' gradient of 777 x 1000 x 504
 // made of them was up to 2.8e-5 of its norm away.)
 __device__ __forceinline__ float silu_backward_exact(float d, float z) {
