@@ -299,21 +299,19 @@ def _plain_route(s):
         if c["renorm"]:
             w = torch.where(none, 0.0, w)
             w = w / w.sum(1, keepdim=True)
-    w = torch.where(none, 0.0, w * c["scale"])
+    w = torch.where(none, 0.0, w)           # before the scale
     s["idx"].copy_(torch.where(none, -1, idx))
-    s["w"].copy_(w)
+    s["w"].copy_(w * c["scale"])
     if not c["train"]:
         return s["idx"], s["w"]
     # a choice that is missing has weight 0 and adds nothing
-    at, dw = s["idx"].clamp(min=0), torch.where(none, 0.0, s["dw"])
-    mean = (dw * w).sum(1, keepdim=True)
+    at, dw = s["idx"].clamp(min=0), torch.where(none, 0.0, s["dw"] * c["scale"])
     if c["score"] == "softmax" and not c["renorm"]:
         p = torch.where(l > -math.inf, torch.exp(l - top) / torch.exp(over - top).sum(1, keepdim=True), 0.0)
-        d = (-p * mean).scatter_add(1, at, dw * w)
+        d = (-p * (dw * w).sum(1, keepdim=True)).scatter_add(1, at, dw * w)
     else:
-        d = dw * w
-        if c["renorm"]:
-            d = d - w * mean / c["scale"]
+        # sum_i w_i (dw_j - dw_i): exactly 0 where one choice has all the weight
+        d = w * ((dw[:, :, None] - dw[:, None, :]) * w[:, None, :]).sum(2) if c["renorm"] else dw * w
         if c["score"] == "sigmoid":
             d = d / (1 + torch.exp(chosen))
         d = torch.zeros_like(l).scatter_add(1, at, torch.where(none, 0.0, d))
@@ -353,9 +351,10 @@ def _plain_norm(s):
 
 def _round_rows(x):
     """Codes and scales of rows: the quotients are rounded in 64 bits, where a border is a border."""
-    x = x.float()
-    scale = x.abs().amax(1).clamp(min=2.0 ** -100) / 127
-    return torch.round(x.double() / scale.double()[:, None]).float(), scale
+    x = x.double()
+    a = x.abs().amax(1).clamp(min=2.0 ** -100)
+    scale = (a / torch.full_like(a, 127)).float()   # a true quotient, rounded once
+    return torch.round(x / scale.double()[:, None]).float(), scale
 
 
 def _act(z, act):
