@@ -20,6 +20,8 @@ EP_FP8_E4M3 = 1
 EP_FP8_E4M3_POW2 = 2
 EP_MXFP8_E4M3 = 3
 EP_F16 = 4
+EP_INT8 = 6
+EP_F32 = 7                   # the router's logits only
 EP_SCALES_MN_MAJOR = 0x100   # OR-ed into an FP8 dtype: scales stored transposed
 EP_READ_X_AHEAD = 0x200      # OR-ed into ep_layout_dispatch's dtype: x read into the MALL during the layout
 EP_GRAD_F32 = 0x400          # OR-ed into a weights' gradient's dtype: fp32 gradients
@@ -29,6 +31,8 @@ EP_ACT_RELU = 1
 EP_ACT_GELU = 2
 EP_ACT_SILU = 3
 EP_ACT_SWIGLU = 4
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
 _FP8_DTYPES = (EP_FP8_E4M3, EP_FP8_E4M3_POW2, EP_MXFP8_E4M3)
 EP_FLAG_BAD_EXPERT = 1
 EP_FLAG_OVERFLOW = 2
@@ -61,9 +65,24 @@ class ep_layout_t(ctypes.Structure):
     ]
 
 
+class ep_router_t(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 # name -> (restype, argtypes), mirroring include/ep.h
 _i64, _i32, _u32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t
 _LP = ctypes.POINTER(ep_layout_t)
+_RP = ctypes.POINTER(ep_router_t)
+_f32 = ctypes.c_float
 SIGNATURES = {
     "ep_layout_init": (ctypes.c_int, [_LP, _i64, _i32, _i32, _i32, _i32]),
     "ep_num_recv_rows": (_i64, [_i64, _i32, _i32, _i32]),
@@ -93,6 +112,14 @@ SIGNATURES = {
     "ep_linear_grad_w": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]),
     "ep_act_grad": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
     "ep_combine_grad": (ctypes.c_int, [_vp, _vp, _vp, _LP, _i32, _i32, _vp, _vp, _vp]),
+    "ep_quantize_int8": (ctypes.c_int, [_vp, _LP, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "ep_linear_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "ep_route": (ctypes.c_int, [_vp, _vp, _i64, _RP, _i32, _vp, _vp, _vp]),
+    "ep_route_grad": (ctypes.c_int, [_vp, _vp, _vp, _i64, _RP, _i32, _vp, _vp]),
+    "ep_block_norm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _f32, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp]),
+    "ep_block_norm_grad_workspace_bytes": (_sz, [_i64, _i32]),
+    "ep_block_norm_grad": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i64, _i32, _i32, _f32,
+                                          _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ep_version": (ctypes.c_char_p, []),
 }
@@ -250,6 +277,8 @@ def _dispatch_types(recv_dtype: int):
     """(x dtype, recv_x dtype, recv_scales dtype) of a receive dtype (with or
     without EP_SCALES_MN_MAJOR)."""
     recv_dtype &= ~(EP_SCALES_MN_MAJOR | EP_READ_X_AHEAD)
+    if recv_dtype == EP_INT8:
+        return torch.bfloat16, torch.int8, torch.float32
     if recv_dtype == EP_F16:
         return torch.float16, torch.float16, None
     if recv_dtype == EP_MXFP8_E4M3:
@@ -260,7 +289,10 @@ def _dispatch_types(recv_dtype: int):
 
 
 def _check_scales(recv_dtype: int, recv_scales, R: int, H: int) -> None:
-    """Every FP8 scale layout holds H/128 four-byte words per receive row."""
+    """Every FP8 scale layout holds H/128 four-byte words per receive row; int8 rows have one scale."""
+    if (recv_dtype & ~EP_READ_X_AHEAD) == EP_INT8 and recv_scales is not None:
+        if tuple(recv_scales.shape) != (R,):
+            raise ValueError("recv_scales must have shape %s" % ((R,),))
     if (recv_dtype & ~(EP_SCALES_MN_MAJOR | EP_READ_X_AHEAD)) in _FP8_DTYPES and recv_scales is not None:
         if recv_scales.numel() * recv_scales.element_size() != R * (H // 128) * 4:
             raise ValueError("recv_scales does not hold %d rows of %d channels' scales" % (R, H))
@@ -271,7 +303,8 @@ def ep_dispatch(x: torch.Tensor, layout: EpLayout, recv_dtype: int, recv_x: torc
     """x bf16 [T, H] -> recv_x: bf16 [R, H]; uint8 [R, H] FP8 codes with
     recv_scales fp32 [R, H/128] (EP_FP8_E4M3, EP_FP8_E4M3_POW2) or uint8
     [R, H/32] E8M0 bytes (EP_MXFP8_E4M3), or their transposes [H/128, R] and
-    [H/32, R] with EP_SCALES_MN_MAJOR.  EP_F16: x and recv_x fp16."""
+    [H/32, R] with EP_SCALES_MN_MAJOR.  EP_F16: x and recv_x fp16.  EP_INT8:
+    recv_x int8 with recv_scales fp32 [R]."""
     T, H = layout.num_tokens, x.shape[-1]
     if tuple(x.shape) != (T, H) or tuple(recv_x.shape) != (layout.num_recv_rows, H):
         raise ValueError("dispatch buffers do not match the layout")
@@ -482,7 +515,8 @@ def ep_expert_gemm(x: torch.Tensor, weights: torch.Tensor, layout: EpLayout, out
     act(x W_e^T + bias_e) for the rows of each expert e; W = N, or 2N for EP_ACT_SWIGLU.
     bf16 / fp16: all of that type.  FP8: uint8 codes, x_scales fp32 [R, K/128] ([K/128, R] with
     EP_SCALES_MN_MAJOR), weight_scales fp32 [E, W/128, K/128].  MXFP8: x_scales uint8 [R, K/32],
-    weight_scales uint8 [E, W, K/32].  FP8 results are bf16.  preact [R, W]: the product itself."""
+    weight_scales uint8 [E, W, K/32].  INT8: int8 codes, x_scales fp32 [R], weight_scales fp32
+    [E, W].  FP8 and INT8 results are bf16.  preact [R, W]: the product itself."""
     c = _Call(x, "x", 2, layout)
     R, E, K, N = layout.num_recv_rows, layout.num_experts, x.shape[1], out.shape[-1]
     W, base = _width(N, act), dtype & ~EP_SCALES_MN_MAJOR
@@ -492,6 +526,8 @@ def ep_expert_gemm(x: torch.Tensor, weights: torch.Tensor, layout: EpLayout, out
         st = torch.uint8 if mx else torch.float32
         xs = (R, K // 32) if mx else (K // 128, R) if dtype & EP_SCALES_MN_MAJOR else (R, K // 128)
         ws = (E, W, K // 32) if mx else (E, W // 128, K // 128)
+    elif dtype == EP_INT8:
+        qt, st, xs, ws = torch.int8, torch.float32, (R,), (E, W)
     else:
         qt, st, xs, ws = et, torch.float32, (), ()
         if x_scales is not None or weight_scales is not None:
@@ -568,6 +604,141 @@ def ep_linear_grad_w(dy: torch.Tensor, x: torch.Tensor, dweights: torch.Tensor, 
     gt = torch.float32 if dtype & EP_GRAD_F32 else et
     c.run("ep_linear_grad_w", stream, c.operand(dy, "dy", et, (T, N)), c.operand(x, "x", et, (T, K)), T, K, N,
           dtype, c.output(dweights, "dweights", gt, (N, K)), c.output(dbias, "dbias", gt, (N,)))
+
+
+def ep_quantize_int8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, dtype: int,
+                     layout: EpLayout | None = None, stream=None) -> None:
+    """x [rows, n] (bf16, or fp16 with EP_F16) -> q int8 [rows, n] and scales fp32 [rows], one for
+    each row; with a layout, its used receive rows alone (rows = R)."""
+    c = _Call(x, "x", 2, layout)
+    rows, n, et = x.shape[0], x.shape[1], _elem(dtype)
+    if layout is not None and rows != layout.num_recv_rows:
+        raise ValueError("x must have the layout's %d receive rows" % layout.num_recv_rows)
+    c.run("ep_quantize_int8", stream, c.operand(x, "x", et, (rows, n)),
+          None if layout is None else ctypes.byref(layout.struct), rows, n, dtype,
+          c.output(q, "q", torch.int8, (rows, n)), c.output(scales, "scales", torch.float32, (rows,)))
+
+
+def ep_linear_int8(x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
+                   weight_scales: torch.Tensor, out: torch.Tensor, act: int = EP_ACT_NONE,
+                   bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   preact: torch.Tensor | None = None, stream=None) -> None:
+    """ep_linear on codes: x int8 [rows, K] and x_scales fp32 [rows], weights int8 [W, K] and
+    weight_scales fp32 [W]; bias, residual, preact and out bf16."""
+    c = _Call(x, "x", 2)
+    T, K, N, et = x.shape[0], x.shape[1], out.shape[-1], torch.bfloat16
+    W = _width(N, act)
+    res = c.operand(residual, "residual", et, (T, N))
+    c.run("ep_linear_int8", stream, c.operand(x, "x", torch.int8, (T, K)),
+          c.operand(x_scales, "x_scales", torch.float32, (T,)),
+          c.operand(weights, "weights", torch.int8, (W, K)),
+          c.operand(weight_scales, "weight_scales", torch.float32, (W,)),
+          c.operand(bias, "bias", et, (W,)), res, T, K, N, act, c.output(preact, "preact", et, (T, W)),
+          c.output(out, "out", et, (T, N), may_be=("residual",)))
+
+
+class EpRouter:
+    """How a router chooses (ep_router_t): the handle of ep_route and ep_route_grad."""
+
+    def __init__(self, num_experts: int, num_topk: int, score: int = EP_SCORE_SOFTMAX, num_groups: int = 1,
+                 topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+        self.struct = ep_router_t(num_experts, num_topk, score, num_groups, topk_groups, group_top,
+                                  int(renormalize), scale)
+        # the library's own checks, on a call with nothing to do
+        _check("ep_route", lib().ep_route(None, None, 0, ctypes.byref(self.struct), EP_F32, None, None, None))
+
+    @property
+    def num_experts(self) -> int:
+        return self.struct.num_experts
+
+    @property
+    def num_topk(self) -> int:
+        return self.struct.num_topk
+
+
+def _logits_type(dtype: int) -> torch.dtype:
+    return torch.float32 if dtype == EP_F32 else _elem(dtype)
+
+
+def ep_route(logits: torch.Tensor, router: EpRouter, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+             dtype: int, bias: torch.Tensor | None = None, stream=None) -> None:
+    """logits [T, E] (fp32, bf16 or fp16, as dtype says) and bias fp32 [E] -> topk_idx int64 [T, k]
+    (-1: none) and topk_weights fp32 [T, k], what ep_get_layout and ep_combine take."""
+    c = _Call(logits, "logits", 2)
+    T, E, k = logits.shape[0], router.num_experts, router.num_topk
+    c.run("ep_route", stream, c.operand(logits, "logits", _logits_type(dtype), (T, E)),
+          c.operand(bias, "bias", torch.float32, (E,)), T, ctypes.byref(router.struct), dtype,
+          c.output(topk_idx, "topk_idx", torch.int64, (T, k)),
+          c.output(topk_weights, "topk_weights", torch.float32, (T, k)))
+
+
+def ep_route_grad(d_topk_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                  router: EpRouter, d_logits: torch.Tensor, dtype: int, stream=None) -> None:
+    """d_topk_weights fp32 [T, k] (what ep_combine_grad gives), ep_route's logits and topk_idx ->
+    d_logits [T, E] of logits' type."""
+    c = _Call(logits, "logits", 2)
+    T, E, k, lt = logits.shape[0], router.num_experts, router.num_topk, _logits_type(dtype)
+    c.run("ep_route_grad", stream, c.operand(d_topk_weights, "d_topk_weights", torch.float32, (T, k)),
+          c.operand(logits, "logits", lt, (T, E)), c.operand(topk_idx, "topk_idx", torch.int64, (T, k)), T,
+          ctypes.byref(router.struct), dtype, c.output(d_logits, "d_logits", lt, (T, E)))
+
+
+def ep_block_norm(y: torch.Tensor | None, residual: torch.Tensor | None, out: torch.Tensor | None,
+                  dtype: int, eps: float = 1e-6, post_weight: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                  pre_weight: torch.Tensor | None = None, normed: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """x = residual_scale residual + gate norm(y) post_weight -> out; norm(x) pre_weight -> normed.
+    y, residual, out, normed [rows, H], weights [H], gate fp32 [rows].  Without post_weight y is
+    not normed; y or residual, and out or pre_weight with normed, may be left out.  out or normed
+    may be y or residual."""
+    first, name = (residual, "residual") if y is None else (y, "y")
+    if first is None:
+        raise ValueError("y or residual is needed")
+    c = _Call(first, name, 2)
+    shape, et = tuple(first.shape), _elem(dtype)
+    H = shape[1]
+    args = (c.operand(y, "y", et, shape), c.operand(post_weight, "post_weight", et, (H,)),
+            c.operand(gate, "gate", torch.float32, (shape[0],)), c.operand(residual, "residual", et, shape),
+            residual_scale, c.operand(pre_weight, "pre_weight", et, (H,)), shape[0], H, dtype, eps)
+    rows = ("y", "residual")
+    c.run("ep_block_norm", stream, *args, c.output(out, "out", et, shape, may_be=rows),
+          c.output(normed, "normed", et, shape, may_be=rows))
+
+
+def ep_block_norm_grad_workspace_bytes(rows: int, hidden: int) -> int:
+    return int(lib().ep_block_norm_grad_workspace_bytes(rows, hidden))
+
+
+def ep_block_norm_grad(d_out: torch.Tensor | None, d_normed: torch.Tensor | None, y: torch.Tensor | None,
+                       residual: torch.Tensor | None, dtype: int, workspace: torch.Tensor | None = None,
+                       eps: float = 1e-6, post_weight: torch.Tensor | None = None,
+                       gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                       pre_weight: torch.Tensor | None = None, d_y: torch.Tensor | None = None,
+                       d_residual: torch.Tensor | None = None, d_gate: torch.Tensor | None = None,
+                       d_post_weight: torch.Tensor | None = None, d_pre_weight: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """Gradients of ep_block_norm from d_out and d_normed [rows, H] (either may be left out) and its
+    inputs; every gradient may be left out.  Weights' gradients have dtype's type or, with
+    EP_GRAD_F32, fp32 (EP_GRAD_ACCUMULATE adds), and need a uint8 workspace of
+    ep_block_norm_grad_workspace_bytes.  d_y and d_residual may be d_out or d_normed."""
+    first, name = (d_normed, "d_normed") if d_out is None else (d_out, "d_out")
+    if first is None:
+        raise ValueError("d_out or d_normed is needed")
+    c = _Call(first, name, 2)
+    shape, et = tuple(first.shape), _elem(dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE))
+    T, H = shape
+    gt = torch.float32 if dtype & EP_GRAD_F32 else et
+    args = (c.operand(d_out, "d_out", et, shape), c.operand(d_normed, "d_normed", et, shape),
+            c.operand(y, "y", et, shape), c.operand(post_weight, "post_weight", et, (H,)),
+            c.operand(gate, "gate", torch.float32, (T,)), c.operand(residual, "residual", et, shape),
+            residual_scale, c.operand(pre_weight, "pre_weight", et, (H,)), T, H, dtype, eps)
+    size = 0 if workspace is None else workspace.numel()
+    rows = ("d_out", "d_normed")
+    c.run("ep_block_norm_grad", stream, *args, c.output(d_y, "d_y", et, shape, may_be=rows),
+          c.output(d_residual, "d_residual", et, shape, may_be=rows), c.output(d_gate, "d_gate", torch.float32, (T,)),
+          c.output(d_post_weight, "d_post_weight", gt, (H,)), c.output(d_pre_weight, "d_pre_weight", gt, (H,)),
+          c.output(workspace, "workspace", torch.uint8, (size,)), size)
 
 
 def ep_act_grad(dy: torch.Tensor, preact: torch.Tensor, dz: torch.Tensor, dtype: int, act: int,

@@ -6,7 +6,10 @@
 #include <mutex>
 
 #include "ep_gemm.h"
+#include "ep_int8.h"
 #include "ep_internal.h"
+#include "ep_norm.h"
+#include "ep_route.h"
 
 namespace {
 
@@ -97,16 +100,17 @@ void* scratch_on_current_device() {
 int check_dispatch(const void* x, const ep_layout_t* layout, int32_t hidden, int32_t recv_dtype,
                    void* recv_x, void* recv_scales, bool read_ahead_ok) {
   const int32_t base = ep::dtype_base(recv_dtype);
-  const bool fp8 = ep::dtype_is_fp8(base);
-  if (base != EP_BF16 && base != EP_F16 && !fp8) return EP_ERR_DTYPE;
+  const bool fp8 = ep::dtype_is_fp8(base), scaled = ep::dtype_has_scales(base);
+  if (base != EP_BF16 && base != EP_F16 && !scaled) return EP_ERR_DTYPE;
   if (ep::dtype_scales_mn(recv_dtype) && !fp8) return EP_ERR_DTYPE;
   if (ep::dtype_read_x_ahead(recv_dtype) && !read_ahead_ok) return EP_ERR_DTYPE;
-  if (hidden < 8 || hidden > EP_MAX_HIDDEN || hidden % 8 != 0 || (fp8 && hidden % 128 != 0))
+  if (hidden < 8 || hidden > EP_MAX_HIDDEN || hidden % 8 != 0 || (fp8 && hidden % 128 != 0) ||
+      (base == EP_INT8 && hidden % 16 != 0))
     return EP_ERR_SHAPE;
   if (layout->num_tokens == 0) return EP_OK;
-  if (x == nullptr || recv_x == nullptr || (fp8 && recv_scales == nullptr)) return EP_ERR_NULL;
+  if (x == nullptr || recv_x == nullptr || (scaled && recv_scales == nullptr)) return EP_ERR_NULL;
   if (!aligned16(x) || !aligned16(recv_x) ||
-      (fp8 && (reinterpret_cast<uintptr_t>(recv_scales) & 3u) != 0))
+      (scaled && (reinterpret_cast<uintptr_t>(recv_scales) & 3u) != 0))
     return EP_ERR_ALIGN;
   return EP_OK;
 }
@@ -136,22 +140,23 @@ int dense_group(int64_t rows, ep::RowGroups* g) {
   return EP_OK;
 }
 
-// Forward of ep_expert_gemm and ep_linear.
+// Forward of ep_expert_gemm, ep_linear and ep_linear_int8.
 int forward(ep::GemmArgs& g, const void* x, const void* x_scales, const void* w,
             const void* w_scales, int32_t in_f, int32_t out_f, int32_t dtype, void* stream) {
   const int32_t base = ep::dtype_base(dtype);
-  const bool fp8 = ep::dtype_is_fp8(base);
-  if ((base != EP_BF16 && base != EP_F16 && !fp8) || ep::dtype_read_x_ahead(dtype) || !known_act(g.act))
+  const bool fp8 = ep::dtype_is_fp8(base), int8 = base == EP_INT8, scaled = fp8 || int8;
+  if ((base != EP_BF16 && base != EP_F16 && !scaled) || ep::dtype_read_x_ahead(dtype) || !known_act(g.act))
     return EP_ERR_DTYPE;
   if (ep::dtype_scales_mn(dtype) && base != EP_FP8_E4M3 && base != EP_FP8_E4M3_POW2)
     return EP_ERR_DTYPE;
-  if (!feature_size(in_f, fp8 ? 128 : 8) || !feature_size(out_f, fp8 ? 128 : 8)) return EP_ERR_SHAPE;
+  if (!feature_size(in_f, fp8 ? 128 : int8 ? 16 : 8) || !feature_size(out_f, fp8 ? 128 : 8))
+    return EP_ERR_SHAPE;
   if (g.groups.rows == 0) return EP_OK;
   if (x == nullptr || w == nullptr || g.out == nullptr ||
-      (fp8 && (x_scales == nullptr || w_scales == nullptr)))
+      (scaled && (x_scales == nullptr || w_scales == nullptr)))
     return EP_ERR_NULL;
   if (!aligned16(x) || !aligned16(w) || !aligned16(g.bias) || !aligned16(g.residual) ||
-      !aligned16(g.preact) || !aligned16(g.out) || (fp8 && (!aligned4(x_scales) || !aligned4(w_scales))))
+      !aligned16(g.preact) || !aligned16(g.out) || (scaled && (!aligned4(x_scales) || !aligned4(w_scales))))
     return EP_ERR_ALIGN;
   const int32_t width = g.act == EP_ACT_SWIGLU ? 2 * out_f : out_f;
   g.a = x;
@@ -159,10 +164,11 @@ int forward(ep::GemmArgs& g, const void* x, const void* x_scales, const void* w,
   g.lda = g.ldb = g.reduce = in_f;
   g.out_cols = out_f;
   g.b_stride = (int64_t)width * in_f;
+  g.a_scales = x_scales;
+  g.b_scales = w_scales;
+  if (int8) return launch_status(ep::launch_gemm_int8(g, static_cast<hipStream_t>(stream)));
   if (fp8) {
     const bool mn = ep::dtype_scales_mn(dtype);
-    g.a_scales = x_scales;
-    g.b_scales = w_scales;
     g.a_scale_row = mn ? 1 : in_f / 128;
     g.a_scale_step = mn ? g.groups.rows : 1;
     return launch_status(ep::launch_gemm_fp8(g, base == EP_MXFP8_E4M3, static_cast<hipStream_t>(stream)));
@@ -204,6 +210,31 @@ int weights_grad(ep::GemmArgs& g, const void* dy, const void* x, int32_t in_f, i
   g.grad_f32 = (dtype & EP_GRAD_F32) != 0;
   g.accumulate = (dtype & EP_GRAD_ACCUMULATE) != 0;
   return launch_status(ep::launch_gemm(g, 2, base == EP_F16, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// The router and the block norms.
+int check_router(const ep_router_t* r, int64_t tokens, int32_t dtype, ep::RouteArgs* a) {
+  if (r == nullptr) return EP_ERR_NULL;
+  if ((dtype != EP_F32 && dtype != EP_BF16 && dtype != EP_F16) ||
+      (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID))
+    return EP_ERR_DTYPE;
+  const int32_t E = r->num_experts, k = r->num_topk, G = r->num_groups;
+  if (E < 1 || E > EP_MAX_EXPERTS || k < 1 || k > EP_MAX_TOPK || G < 1 || E % G != 0 ||
+      r->topk_groups < 1 || r->topk_groups > G || k > r->topk_groups * (E / G) ||
+      r->group_top < 1 || r->group_top > 2 || r->group_top > E / G || tokens < 0 ||
+      tokens > kInt32Limit / k)
+    return EP_ERR_SHAPE;
+  *a = ep::RouteArgs{E, k, G, r->topk_groups, r->group_top, r->score == EP_SCORE_SOFTMAX,
+                     r->renormalize != 0, r->scale, 0, 0};
+  return EP_OK;
+}
+
+int check_norm(int64_t rows, int32_t hidden, int32_t dtype, float eps) {
+  if (dtype != EP_BF16 && dtype != EP_F16) return EP_ERR_DTYPE;
+  if (rows < 0 || rows > kInt32Limit || !feature_size(hidden, 8) || !(eps > 0.0f && eps <= 3.4e38f))
+    return EP_ERR_SHAPE;
+  return EP_OK;
 }
 
 }  // namespace
@@ -275,7 +306,7 @@ int ep_layout_dispatch(const int64_t* topk_idx, const ep_layout_t* layout, void*
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool read_ahead = ep::dtype_read_x_ahead(recv_dtype);
   recv_dtype &= ~EP_READ_X_AHEAD;
-  if (ep::fused_layout_dispatch_fits(*layout))
+  if (recv_dtype != EP_INT8 && ep::fused_layout_dispatch_fits(*layout))
     return launch_status(ep::launch_layout_dispatch_small(topk_idx, *layout, x, hidden, recv_dtype,
                                                           recv_x, recv_scales, s));
   // With EP_READ_X_AHEAD the layout's launches also read x (2-byte elements)
@@ -462,6 +493,35 @@ int ep_linear(const void* x, const void* weights, const void* bias, const void* 
   return forward(g, x, nullptr, weights, nullptr, in_features, out_features, dtype, stream);
 }
 
+int ep_linear_int8(const void* x, const float* x_scales, const void* weights,
+                   const float* weight_scales, const void* bias, const void* residual, int64_t rows,
+                   int32_t in_features, int32_t out_features, int32_t act, void* preact, void* out,
+                   void* stream) {
+  ep::GemmArgs g = {};
+  const int rc = dense_group(rows, &g.groups);
+  if (rc != EP_OK) return rc;
+  g.act = act;
+  g.bias = bias;
+  g.residual = residual;
+  g.preact = preact;
+  g.out = out;
+  return forward(g, x, x_scales, weights, weight_scales, in_features, out_features, EP_INT8, stream);
+}
+
+int ep_quantize_int8(const void* x, const ep_layout_t* layout, int64_t rows, int32_t n,
+                     int32_t dtype, void* q, float* scales, void* stream) {
+  ep::RowGroups groups;
+  const int rc = layout != nullptr ? layout_groups(layout, &groups) : dense_group(rows, &groups);
+  if (rc != EP_OK) return rc;
+  if (dtype != EP_BF16 && dtype != EP_F16) return EP_ERR_DTYPE;
+  if (groups.rows != rows || n < 16 || !feature_size(n, 16)) return EP_ERR_SHAPE;
+  if (rows == 0) return EP_OK;
+  if (x == nullptr || q == nullptr || scales == nullptr) return EP_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scales)) return EP_ERR_ALIGN;
+  return launch_status(ep::launch_quantize_int8(x, groups, n, dtype == EP_F16, q, scales,
+                                                static_cast<hipStream_t>(stream)));
+}
+
 int ep_linear_grad_x(const void* dy, const void* weights, int64_t rows, int32_t in_features,
                      int32_t out_features, int32_t dtype, int32_t act, const void* preact,
                      void* dx, void* stream) {
@@ -514,6 +574,117 @@ int ep_combine_grad(const void* dout, const void* expert_out, const float* topk_
   return launch_status(ep::launch_combine_grad(dout, expert_out, topk_weights, *layout, hidden,
                                                dtype == EP_F16, d_expert_out, d_topk_weights,
                                                static_cast<hipStream_t>(stream)));
+}
+
+int ep_route(const void* logits, const float* bias, int64_t num_tokens, const ep_router_t* router,
+             int32_t dtype, int64_t* topk_idx, float* topk_weights, void* stream) {
+  ep::RouteArgs a;
+  const int rc = check_router(router, num_tokens, dtype, &a);
+  if (rc != EP_OK || num_tokens == 0) return rc;
+  if (logits == nullptr || topk_idx == nullptr || topk_weights == nullptr) return EP_ERR_NULL;
+  if (!aligned16(logits) || !aligned4(bias) || !aligned4(topk_weights) ||
+      (reinterpret_cast<uintptr_t>(topk_idx) & 7u) != 0)
+    return EP_ERR_ALIGN;
+  return launch_status(ep::launch_route(logits, bias, num_tokens, a, dtype, topk_idx, topk_weights,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int ep_route_grad(const float* d_topk_weights, const void* logits, const int64_t* topk_idx,
+                  int64_t num_tokens, const ep_router_t* router, int32_t dtype, void* d_logits,
+                  void* stream) {
+  ep::RouteArgs a;
+  const int rc = check_router(router, num_tokens, dtype, &a);
+  if (rc != EP_OK || num_tokens == 0) return rc;
+  if (d_topk_weights == nullptr || logits == nullptr || topk_idx == nullptr || d_logits == nullptr)
+    return EP_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(d_logits) || !aligned4(d_topk_weights) ||
+      (reinterpret_cast<uintptr_t>(topk_idx) & 7u) != 0)
+    return EP_ERR_ALIGN;
+  return launch_status(ep::launch_route_grad(d_topk_weights, logits, topk_idx, num_tokens, a, dtype,
+                                             d_logits, static_cast<hipStream_t>(stream)));
+}
+
+int ep_block_norm(const void* y, const void* post_weight, const float* gate, const void* residual,
+                  float residual_scale, const void* pre_weight, int64_t rows, int32_t hidden,
+                  int32_t dtype, float eps, void* out, void* normed, void* stream) {
+  const int rc = check_norm(rows, hidden, dtype, eps);
+  if (rc != EP_OK || rows == 0) return rc;
+  if ((y == nullptr && (residual == nullptr || post_weight != nullptr || gate != nullptr)) ||
+      (out == nullptr && normed == nullptr) || (pre_weight == nullptr) != (normed == nullptr))
+    return EP_ERR_NULL;
+  if (!aligned16(y) || !aligned16(post_weight) || !aligned4(gate) || !aligned16(residual) ||
+      !aligned16(pre_weight) || !aligned16(out) || !aligned16(normed))
+    return EP_ERR_ALIGN;
+  ep::NormArgs a = {};
+  a.y = y;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.residual = residual;
+  a.residual_scale = residual_scale;
+  a.pre_weight = pre_weight;
+  a.rows = rows;
+  a.hidden = hidden;
+  a.eps = eps;
+  a.out = out;
+  a.normed = normed;
+  return launch_status(ep::launch_block_norm(a, dtype == EP_F16, static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_block_norm_grad_workspace_bytes(int64_t rows, int32_t hidden) {
+  if (rows < 0 || rows > kInt32Limit || !feature_size(hidden, 8)) return 0;
+  return 2 * sizeof(float) * (size_t)ep::norm_partials(rows, hidden) * (size_t)hidden;
+}
+
+int ep_block_norm_grad(const void* d_out, const void* d_normed, const void* y,
+                       const void* post_weight, const float* gate, const void* residual,
+                       float residual_scale, const void* pre_weight, int64_t rows, int32_t hidden,
+                       int32_t dtype, float eps, void* d_y, void* d_residual, float* d_gate,
+                       void* d_post_weight, void* d_pre_weight, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const int32_t base = dtype & ~(EP_GRAD_F32 | EP_GRAD_ACCUMULATE);
+  const int rc = check_norm(rows, hidden, base, eps);
+  if (rc != EP_OK) return rc;
+  const bool weights = d_post_weight != nullptr || d_pre_weight != nullptr;
+  if (rows == 0 && !weights) return EP_OK;
+  if (rows > 0) {
+    if ((y == nullptr && (residual == nullptr || post_weight != nullptr || gate != nullptr)) ||
+        (d_out == nullptr && d_normed == nullptr) || (pre_weight == nullptr) != (d_normed == nullptr) ||
+        (d_y != nullptr && y == nullptr) || (d_residual != nullptr && residual == nullptr) ||
+        (d_gate != nullptr && gate == nullptr) || (d_post_weight != nullptr && post_weight == nullptr) ||
+        (d_pre_weight != nullptr && pre_weight == nullptr) ||
+        (d_y == nullptr && d_residual == nullptr && d_gate == nullptr && !weights))
+      return EP_ERR_NULL;
+    if (weights && workspace == nullptr) return EP_ERR_NULL;
+  }
+  if (!aligned16(d_out) || !aligned16(d_normed) || !aligned16(y) || !aligned16(post_weight) ||
+      !aligned4(gate) || !aligned16(residual) || !aligned16(pre_weight) || !aligned16(d_y) ||
+      !aligned16(d_residual) || !aligned4(d_gate) || !aligned16(d_post_weight) ||
+      !aligned16(d_pre_weight) || (weights && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return EP_ERR_ALIGN;
+  if (weights && rows > 0 && workspace_bytes < ep_block_norm_grad_workspace_bytes(rows, hidden))
+    return EP_ERR_WORKSPACE;
+  ep::NormArgs a = {};
+  a.y = y;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.residual = residual;
+  a.residual_scale = residual_scale;
+  a.pre_weight = pre_weight;
+  a.rows = rows;
+  a.hidden = hidden;
+  a.eps = eps;
+  a.d_out = d_out;
+  a.d_normed = d_normed;
+  a.d_y = d_y;
+  a.d_residual = d_residual;
+  a.d_gate = d_gate;
+  a.d_post_weight = d_post_weight;
+  a.d_pre_weight = d_pre_weight;
+  a.grad_f32 = (dtype & EP_GRAD_F32) != 0;
+  a.accumulate = (dtype & EP_GRAD_ACCUMULATE) != 0;
+  a.partial = static_cast<float*>(workspace);
+  return launch_status(
+      ep::launch_block_norm_grad(a, base == EP_F16, static_cast<hipStream_t>(stream)));
 }
 
 int ep_dequant_fp8(const uint8_t* q, const float* scales, int64_t rows, int32_t hidden, void* y,

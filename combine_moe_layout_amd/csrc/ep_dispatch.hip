@@ -19,6 +19,7 @@
 // staging copy saves HBM bandwidth ("DeepEP 编址服务深度对抗分析", section 五.1).
 #include "ep_device.h"
 #include "ep_dispatch_token.h"
+#include "ep_int8.h"
 #include "ep_internal.h"
 
 namespace ep {
@@ -101,6 +102,7 @@ hipError_t launch_dispatch(const void* x, const ep_layout_t& L, int32_t hidden, 
   if (T == 0) return hipSuccess;
   const int64_t mn_rows = dtype_scales_mn(dtype) ? L.num_recv_rows : 0;
   dtype = dtype_base(dtype);
+  if (dtype == EP_INT8) return launch_dispatch_int8(x, L, hidden, recv_x, recv_scales, stream);
   const bool fp8 = dtype_is_fp8(dtype);
   uint32_t* sw = static_cast<uint32_t*>(recv_scales);
   const TokenMap m = token_map(fp8 ? hidden / 16 : hidden / 8);

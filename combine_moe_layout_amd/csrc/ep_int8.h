@@ -1,0 +1,20 @@
+// ep_int8.h -- launchers of the 8-bit integer rows (ep_int8.hip) and products
+// (ep_gemm_int8.hip).
+#pragma once
+
+#include "ep_gemm.h"
+#include "ep_lanes.h"
+
+namespace ep {
+
+hipError_t launch_dispatch_int8(const void* x, const ep_layout_t& L, int32_t hidden, void* recv_x,
+                                void* recv_scales, hipStream_t stream);
+
+// The used rows of `groups` (a layout's, or one dense group).
+hipError_t launch_quantize_int8(const void* x, const RowGroups& groups, int32_t n, bool f16, void* q,
+                                float* scales, hipStream_t stream);
+
+// a, b: int8; a_scales [rows] and b_scales [E, columns of the product] fp32.
+hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t stream);
+
+}  // namespace ep

@@ -63,6 +63,9 @@ inline bool dtype_is_fp8(int32_t dtype) {
   return dtype == EP_FP8_E4M3 || dtype == EP_FP8_E4M3_POW2 || dtype == EP_MXFP8_E4M3;
 }
 
+// Dtypes whose rows come with scales.
+inline bool dtype_has_scales(int32_t dtype) { return dtype_is_fp8(dtype) || dtype == EP_INT8; }
+
 // A dispatch dtype splits into its element type and the option flags.
 inline int32_t dtype_base(int32_t dtype) {
   return dtype & ~(EP_SCALES_MN_MAJOR | EP_READ_X_AHEAD);

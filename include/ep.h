@@ -62,13 +62,15 @@ enum ep_status {
     EP_ERR_DTYPE = -6      /* unknown receive dtype, activation or flag */
 };
 
-/* Receive-buffer element types for ep_dispatch. */
+/* Element types: of ep_dispatch's receive buffer, and of what the other calls name. */
 enum ep_dtype {
     EP_BF16 = 0,          /* bf16 rows, a bit copy of x */
     EP_FP8_E4M3 = 1,      /* OCP FP8 E4M3 codes + one fp32 scale per 128 channels */
     EP_FP8_E4M3_POW2 = 2, /* as EP_FP8_E4M3, with each scale a power of two (see ep_dispatch) */
     EP_MXFP8_E4M3 = 3,    /* OCP MXFP8: E4M3 codes + one E8M0 scale byte per 32 channels */
-    EP_F16 = 4            /* fp16 rows: x is fp16 and the rows are a bit copy of it */
+    EP_F16 = 4,           /* fp16 rows: x is fp16 and the rows are a bit copy of it */
+    EP_INT8 = 6,          /* 8-bit integers + one fp32 scale per row */
+    EP_F32 = 7            /* fp32: the router's logits only */
 };
 
 /* Flags OR-ed into the receive dtype.
@@ -93,6 +95,12 @@ enum ep_act {
     EP_ACT_GELU = 2,   /* z * (1 + erf(z / sqrt(2))) / 2 */
     EP_ACT_SILU = 3,   /* z / (1 + exp(-z)) */
     EP_ACT_SWIGLU = 4  /* silu(z[j]) * z[n + j], j < n */
+};
+
+/* Scores of the router. */
+enum ep_score {
+    EP_SCORE_SOFTMAX = 0, /* exp(l_e) / sum over all experts */
+    EP_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
 };
 
 /* Bits of layout->error_flags, written by ep_get_layout. */
@@ -212,6 +220,8 @@ int ep_get_layout_noalloc(const int64_t* topk_idx, const ep_layout_t* layout, vo
  *                an all-zero block), byte = se + 127, code = nearest E4M3 (ties
  *                to even) of clamp(x / 2^se, -448, 448); requires hidden % 128 == 0.
  *   EP_F16:      x is fp16 [T, hidden] and recv_x fp16 [R, hidden], a bit copy.
+ *   EP_INT8:     recv_x int8 [R, hidden] and recv_scales fp32 [R], the codes and
+ *                scale of ep_quantize_int8; requires hidden % 16 == 0.
  * FP8 dtype | EP_SCALES_MN_MAJOR: the same codes and scale values, with the
  *                scales stored transposed: fp32 [hidden/128, R] (E8M0 bytes
  *                [hidden/32, R] for MXFP8), entry c of receive row r at
@@ -250,6 +260,7 @@ int ep_scales_to_mn_major(const void* scales, int64_t rows, int32_t hidden, int3
  * Layout and dispatch in one call: the same results as ep_get_layout followed
  * by ep_dispatch with the same arguments.  For decode-sized batches -- at most
  * 4096 (token, k) pairs and top-k at most 8 -- both run in a single launch
+ * (not with EP_INT8)
  * (the pages' low-latency mode: "DeepEP是什麼？…" (yololab.net), section
  * "高吞吐與低延遲工作負載"); larger batches run the two calls' kernels in turn.
  * Arguments, layouts and status codes are those of ep_get_layout and
@@ -414,11 +425,14 @@ int ep_combine_groups(const void* z, const ep_layout_t* group_layout, int32_t hi
  *   EP_MXFP8_E4M3: weights E4M3 codes, x_scales E8M0 [R, in_features/32],
  *     weight_scales E8M0 [E, W, in_features/32]; bias, out bf16 (no
  *     EP_SCALES_MN_MAJOR: EP_ERR_DTYPE).
+ *   EP_INT8: weights int8, x_scales fp32 [R], weight_scales fp32 [E, W], one per
+ *     output channel; bias, out bf16.  The codes' products are summed exactly in
+ *     32-bit integers, and the sum is then scaled by both in fp32.
  * bias [E, W], may be NULL.  preact [R, W], may be NULL: z rounded to out's
  * type, what the gradients need.  Rows that no pair uses are neither read nor
  * written, as with ep_dispatch, in the contiguous and the padded layout.
  * in_features and out_features: 8 to EP_MAX_HIDDEN and multiples of 8, with
- * an FP8 dtype of 128.  Pointers 16-byte aligned (scales 4).  out and preact
+ * an FP8 dtype of 128; with EP_INT8 in_features a multiple of 16.  Pointers 16-byte aligned (scales 4).  out and preact
  * must not overlap the inputs.
  * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
  */
@@ -507,6 +521,122 @@ int ep_act_grad(const void* dy, const void* preact, int64_t rows, int32_t n, int
 int ep_combine_grad(const void* dout, const void* expert_out, const float* topk_weights,
                     const ep_layout_t* layout, int32_t hidden, int32_t dtype, void* d_expert_out,
                     float* d_topk_weights, void* stream);
+
+/*
+ * Rows in 8-bit integers with one fp32 scale each (what EP_INT8 products take; for
+ * weights, whose rows are output channels, as well as for activations):
+ *   a = max(max_c |x[r, c]|, 2^-100),  scales[r] = a / 127  (one fp32 division)
+ *   q[r, c] = the integer nearest to x[r, c] / scales[r], ties to even
+ * A row that holds a NaN or an infinity gets a scale of NaN and codes of 0.
+ * x [rows, n] of dtype EP_BF16 or EP_F16; q int8 [rows, n]; scales fp32 [rows].
+ * layout: NULL, or a filled layout, whose receive rows x are (rows =
+ * num_recv_rows): rows that no pair uses are then neither read nor written.
+ * n: 16 to EP_MAX_HIDDEN, a multiple of 16.  x and q 16-byte aligned, not overlapping.
+ * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
+ */
+int ep_quantize_int8(const void* x, const ep_layout_t* layout, int64_t rows, int32_t n,
+                     int32_t dtype, void* q, float* scales, void* stream);
+
+/*
+ * ep_linear on 8-bit integers: z = (x x_scales) (weights weight_scales)^T + bias,
+ * out = act(z) + residual.  x int8 [rows, in_features], x_scales fp32 [rows], weights
+ * int8 [W, in_features], weight_scales fp32 [W]; bias, residual, preact, out bf16, as in
+ * ep_linear.  in_features: a multiple of 16.  Status codes as ep_expert_gemm.
+ */
+int ep_linear_int8(const void* x, const float* x_scales, const void* weights,
+                   const float* weight_scales, const void* bias, const void* residual, int64_t rows,
+                   int32_t in_features, int32_t out_features, int32_t act, void* preact, void* out,
+                   void* stream);
+
+/*
+ * The router's choice: what ep_get_layout's topk_idx and ep_combine's topk_weights are made
+ * of ([yololab] stage table: the gate's top-k index and weights come before dispatch).
+ */
+typedef struct ep_router {
+    int32_t num_experts;  /* E */
+    int32_t num_topk;     /* k */
+    int32_t score;        /* EP_SCORE_* */
+    int32_t num_groups;   /* groups of E / num_groups neighbouring experts; 1: no groups */
+    int32_t topk_groups;  /* groups that a token may choose from, 1 to num_groups */
+    int32_t group_top;    /* a group's score: its largest key (1), or the sum of its two largest (2) */
+    int32_t renormalize;  /* 1: the chosen scores are divided by their sum */
+    float scale;          /* the weights' factor */
+} ep_router_t;
+
+/*
+ * For every token t, with s = the scores of logits[t] and key = s + bias (without a
+ * bias the logits themselves, which order the experts alike):
+ *   1. the topk_groups groups of the largest group scores stay (all, if topk_groups ==
+ *      num_groups); with group_top 2 and no bias a group's score is of s, not of logits;
+ *   2. topk_idx[t] = the experts of the k largest keys among those groups, descending;
+ *   3. topk_weights[t, j] = scale * s[topk_idx[t, j]], renormalised if asked for.
+ * The bias (for balance) takes part in the choice alone.  Keys are compared as real numbers,
+ * not as rounded to fp32; equal ones go to the lower index (of experts, of groups).
+ * An expert with a logit of -inf or NaN, or a key of -inf or NaN, is never chosen and has a
+ * score of 0; a logit of +inf counts as the largest fp32 value.  Where a token has fewer
+ * than k experts to choose from, the last entries are -1 (unrouted) with a weight of 0.
+ * logits [T, E] of dtype EP_F32, EP_BF16 or EP_F16; bias fp32 [E] or NULL; topk_idx int64
+ * and topk_weights fp32 [T, k].  Requires num_groups to divide E, k <= EP_MAX_TOPK and k <=
+ * topk_groups * E / num_groups, group_top 2 only where groups have two experts, T * k below
+ * 2^31.  logits 16-byte aligned.  Outputs must not overlap the inputs.
+ * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE (logits' type, score)
+ * or EP_ERR_LAUNCH.
+ */
+int ep_route(const void* logits, const float* bias, int64_t num_tokens, const ep_router_t* router,
+             int32_t dtype, int64_t* topk_idx, float* topk_weights, void* stream);
+
+/*
+ * Gradient of the weights by the logits, the choice held as it was made:
+ *   d_logits[t] = sum_j d_topk_weights[t, j] * d topk_weights[t, j] / d logits[t]
+ * (ep_combine_grad gives d_topk_weights).  Entries of topk_idx outside [0, E), or whose logit
+ * is -inf or NaN, add nothing, and their d_topk_weights is not used.  d_logits [T, E] has
+ * logits' type; every element is written.  d_topk_weights fp32 [T, k].  Pointers, sizes and
+ * status codes as ep_route.
+ */
+int ep_route_grad(const float* d_topk_weights, const void* logits, const int64_t* topk_idx,
+                  int64_t num_tokens, const ep_router_t* router, int32_t dtype, void* d_logits,
+                  void* stream);
+
+/*
+ * The norm after a block with its gate and residual scale, and the norm before the next
+ * block, in one pass over the rows:
+ *   b = y * (mean(y^2) + eps)^-1/2 * post_weight     (post_weight NULL: b = y)
+ *   x = residual_scale * residual + gate[row] * b    (gate NULL: 1)     -> out
+ *   n = x * (mean(x^2) + eps)^-1/2 * pre_weight                         -> normed
+ * computed in fp32, each output rounded once (n from the unrounded x).  y and residual: one of
+ * them may be NULL, and is then left out (y NULL: no post_weight and no gate either).  out may
+ * be NULL, or pre_weight and normed together.  y, residual, out, normed [rows, hidden],
+ * weights [hidden], of dtype EP_BF16 or EP_F16; gate fp32 [rows].  out or normed may be y or
+ * residual itself.  eps > 0 and finite.  hidden: 8 to EP_MAX_HIDDEN, a multiple of 8; 0 <= rows
+ * < 2^31.  Rows whose sum of squares leaves fp32's range are outside the definition.
+ * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
+ */
+int ep_block_norm(const void* y, const void* post_weight, const float* gate, const void* residual,
+                  float residual_scale, const void* pre_weight, int64_t rows, int32_t hidden,
+                  int32_t dtype, float eps, void* out, void* normed, void* stream);
+
+/* Bytes of device workspace that ep_block_norm_grad needs for weights' gradients; 0 if the
+ * sizes are invalid.  Host only. */
+size_t ep_block_norm_grad_workspace_bytes(int64_t rows, int32_t hidden);
+
+/*
+ * Gradients of ep_block_norm from the gradients d_out and d_normed of its outputs (either may
+ * be NULL: 0; pre_weight goes with d_normed) and its inputs, from which everything else is
+ * computed again:
+ *   d_y, d_residual [rows, hidden] of dtype's type, d_gate fp32 [rows], d_post_weight and
+ *   d_pre_weight [hidden] of dtype's type or, with EP_GRAD_F32, fp32; EP_GRAD_ACCUMULATE adds
+ *   these two to what they hold (both flags as in ep_expert_gemm_grad_w).
+ * Every output may be NULL, and needs its input otherwise.  d_y and d_residual may be d_out or
+ * d_normed itself.  Sums over rows are fp32, in a fixed order.  workspace: needed for
+ * d_post_weight and d_pre_weight, 256-byte aligned, scratch.  Sizes, alignment and status codes
+ * as ep_block_norm, and EP_ERR_WORKSPACE.
+ */
+int ep_block_norm_grad(const void* d_out, const void* d_normed, const void* y,
+                       const void* post_weight, const float* gate, const void* residual,
+                       float residual_scale, const void* pre_weight, int64_t rows, int32_t hidden,
+                       int32_t dtype, float eps, void* d_y, void* d_residual, float* d_gate,
+                       void* d_post_weight, void* d_pre_weight, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /*
  * Identity-expert stand-in for FP8 receive buffers (not part of the path;
