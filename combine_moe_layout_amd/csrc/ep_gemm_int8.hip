@@ -5,11 +5,24 @@
 // The sum is exact: at most 65,536 products of magnitude at most 2^14 in 32 bits.  It is rounded
 // to fp32 once, and the scales, bias, activation and residual follow in fp32.
 //
-// A workgroup of 8 waves makes a tile of 192 rows and 256 columns, 96 x 64 to a wave (64 x 128,
-// 32 x 32 to a wave, where that is too much for the rows there are).  A stage is 128 channels.
-// While the matrix instructions work on stage s, both operands of stage s + 2 come into LDS: it
-// holds three stages of rows and two of the matrix operand, whose fragments of stage s have been
-// in registers since stage s - 1 ended.
+// A workgroup of 8 waves makes a tile of 256 rows and 256 columns, 128 x 64 to a wave (64 x 128,
+// 32 x 32 to a wave, where that is too much for the rows there are).  A stage is 128 channels,
+// walked as two halves of 64 (the matrix instruction's reduction): a wave holds its columns'
+// fragments of one half, and goes through its row blocks with three of theirs read ahead, so
+// that 128 sums and all fragments fit 220 registers.  (Fragments of whole stages, twice, spilled;
+// a spilled register's reload waits for the loads to LDS as well.)
+//
+// LDS holds two stages of rows and three of the matrix operand, all 160 KiB of it.  There is one
+// barrier to a stage, three slots before its end, where its last rows have been read and the next
+// stage has landed: after it the rows of stage s + 2 take the place of those of stage s, and the
+// matrix operand of stage s + 3 that of stage s.  So the matrix, which may come from HBM, is on
+// its way for two stages.
+//
+// The stages of a tile are code without a branch, made for each number of row blocks from 3 to 8:
+// two waves share a matrix unit, and one hides what the other does besides only as long as that is
+// shorter than four matrix instructions.  Branches around the row blocks and loads made the
+// product of 8192^3 470 us; without them it takes 393 (2.8 POP/s; the same matrix instructions
+// alone, without loads and LDS reads, 300).
 #include "ep_int8.h"
 
 namespace ep {
@@ -19,14 +32,11 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
 constexpr int kWaves = 8;
-constexpr int kASlots = 3;   // stages of rows in LDS
-constexpr int kBSlots = 2;   // stages of the matrix operand
+constexpr int kASlots = 2;   // stages of rows in LDS
+constexpr int kBSlots = 3;   // stages of the matrix operand
 constexpr int kStage = 128;  // channels, and bytes, per stage
-
-// Lane 16 q + m holds channels 16 q .. 16 q + 15 (`lo`) and 64 + 16 q .. (`hi`) of row m.
-struct Fragment {
-  i32x4 lo, hi;
-};
+constexpr int kAhead = 3;    // row fragments read ahead
+constexpr int kRing = 4;     // row fragments in registers
 
 template <bool kGlu, int TM, int TN, int WM, int WN>
 struct Int8Gemm {
@@ -40,22 +50,22 @@ struct Int8Gemm {
   static constexpr int kWaveBytes = kLdsBytes / kWaves / 1024 * 1024;
   typedef TileStore<kForward, false, kGlu, TM, TN, WM, WN, kWaveBytes> Store;
   static constexpr int kOutCols = Store::kOutCols;
-  static constexpr int kRing = 4;  // row fragments in registers: two in use, two read ahead
-  static_assert(TM % kRing == 2, "two stages leave the ring where it was");
-  static constexpr int kTurn = TM - 2;  // the row of blocks before which stage s + 1 has landed
-  static constexpr int kLoads = kALoads + kBLoads;
+  static_assert(2 * TM % kRing == 0, "a stage leaves the ring where it was");
 
   const GemmArgs& g;
   char* const lds;
   uint32_t lds0;
   Tile t;
-  int32_t stages, whole, blocks;
+  int32_t stages, whole;  // stages, and those of 128 channels
+  int32_t blocks;         // row blocks of a wave that any wave has
+  int32_t a_loads;        // loads of rows of a wave and stage
   const char *a0, *b0;
   uint32_t a_off[kALoads], b_off[kBLoads];
   uint32_t a_read, b_read;
-  int wm, wn, lane, wave, turn;
+  int wm, wn, lane, wave;
   i32x4 acc[TM][TN];
-  Fragment af[kRing], bf[2][TN];
+  // Lane 16 q + m holds channels 16 q .. 16 q + 15 of a half of row m.
+  i32x4 af[kRing], bf[2][TN];
 
   __device__ __forceinline__ Int8Gemm(const GemmArgs& args, char* smem) : g(args), lds(smem) {}
 
@@ -68,17 +78,17 @@ struct Int8Gemm {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
     wn = wave % WN;
-    turn = kTurns == 2 ? wave / 4 : 0;
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
     stages = tiles_of(g.reduce, kStage);
     whole = g.reduce / kStage;
-    blocks = __builtin_amdgcn_readfirstlane(((t.rows + 15) / 16 - wm + WM - 1) / WM);
+    blocks = __builtin_amdgcn_readfirstlane((t.rows + 16 * WM - 1) / (16 * WM));
+    a_loads = (blocks * 2 * WM + kWaves - 1) / kWaves;
     a0 = static_cast<const char*>(g.a) + t.row0 * g.lda;
     // A load brings 8 rows of 128 bytes; 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7), so
-    // that 16 rows read at one chunk touch every bank once.
+    // that 16 rows read at one chunk touch every bank once.  Rows past the last are the last.
 #pragma unroll
     for (int i = 0; i < kALoads; ++i) {
-      const int row = (wave * kALoads + i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+      const int row = a_group(i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
       a_off[i] = (uint32_t)min(row, t.rows - 1) * (uint32_t)g.lda + chunk * 16;
     }
     // A wave loads half of some wave's columns, all gates or all ups: they are neighbours, up to
@@ -87,7 +97,7 @@ struct Int8Gemm {
     b0 = static_cast<const char*>(g.b) + t.e * g.b_stride + (int64_t)base * g.ldb;
 #pragma unroll
     for (int i = 0; i < kBLoads; ++i) {
-      const int row = (wave * kBLoads + i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+      const int row = b_group(i) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
       b_off[i] = (uint32_t)(row_at(row) - base) * (uint32_t)g.ldb + chunk * 16;
     }
     const int q = lane >> 4, m = lane & 15;
@@ -96,88 +106,107 @@ struct Int8Gemm {
     b_read = kBAt + wn * kWaveCols * kStage + in_row;
   }
 
-  // Load j of stage s: of the row operand (into slot `slot`), of the matrix operand.  Chunks past
-  // the end of the reduction are zeros on both sides.
-  __device__ __forceinline__ void load_piece(int s, uint32_t slot, int j) const {
-    const bool of_a = j < kALoads;
-    const int i = of_a ? j : j - kALoads;
-    const char* const from = (of_a ? a0 : b0) + s * kStage;
-    const uint32_t off = of_a ? a_off[of_a ? i : 0] : b_off[of_a ? 0 : i];
-    const uint32_t to = of_a ? lds0 + slot * kABytes + (wave * kALoads + i) * 1024
-                             : lds0 + kBAt + (s & 1) * kBBytes + (wave * kBLoads + i) * 1024;
-    if (s < whole) {
-      load16_to_lds(from, off, to);
+  // Load i of a wave brings rows 8 group .. 8 group + 7 of the operand's part of a stage.
+  __device__ __forceinline__ int a_group(int i) const { return wave + i * kWaves; }
+  __device__ __forceinline__ int b_group(int i) const { return wave * kBLoads + i; }
+  // kWhole: stage s has all its 128 channels; otherwise those past the last are zeros.
+  template <bool kWhole>
+  __device__ __forceinline__ void load(const char* from, uint32_t off, uint32_t to, int s, int group) const {
+    if (kWhole || s < whole) {
+      load16_to_lds(from + s * kStage, off, to);
     } else {
-      const int row = (wave * (of_a ? kALoads : kBLoads) + i) * 8 + (lane >> 3);
+      const int row = group * 8 + (lane >> 3);
       const int channel = s * kStage + (((lane & 7) ^ ((row >> 1) & 7)) * 16);
-      load16_to_lds(channel < g.reduce ? from + off : reinterpret_cast<const char*>(g_zero16), to);
+      load16_to_lds(channel < g.reduce ? from + s * kStage + off : reinterpret_cast<const char*>(g_zero16), to);
     }
   }
-
-  __device__ __forceinline__ Fragment read_fragment(uint32_t offset) const {
-    return Fragment{*reinterpret_cast<const i32x4*>(lds + offset), *reinterpret_cast<const i32x4*>(lds + (offset ^ 64))};
+  template <bool kWhole>
+  __device__ __forceinline__ void load_rows(int s, int i) const {
+    load<kWhole>(a0, a_off[i], lds0 + (s & 1) * kABytes + a_group(i) * 1024, s, a_group(i));
   }
-  __device__ __forceinline__ Fragment row_fragment(uint32_t slot, int i) const {
-    return read_fragment(slot * kABytes + a_read + i * (WM * 16 * kStage));
-  }
-  template <int kSet>
-  __device__ __forceinline__ void read_matrix(uint32_t b_slot, int j) {
-    bf[kSet][j] = read_fragment(b_slot * kBBytes + b_read + j * (16 * kStage));
+  template <bool kWhole>
+  __device__ __forceinline__ void load_matrix(int s, uint32_t slot, int i) const {
+    load<kWhole>(b0, b_off[i], lds0 + kBAt + slot * kBBytes + b_group(i) * 1024, s, b_group(i));
   }
 
-  // Stage s, kSet = s & 1, its rows in slot `now`, those of the next two stages in `next` and
-  // `after`.  Its matrix fragments are in the registers of kSet, its first two row fragments in
-  // af (row block i's in af[(2 kSet + i) % kRing]); the next stage's are read as soon as it has
-  // landed, in the last two row blocks.
-  template <int kSet>
-  __device__ __forceinline__ void step(int s, uint32_t now, uint32_t next, uint32_t after) {
-    // Every wave is done with the rows of stage s - 1, and has the matrix operand of stage s in
-    // registers (the youngest two reads are of this stage's second row fragment).
-    lds_barrier<2>();
-    const bool more2 = s + 2 < stages;
+  // Slot u of a stage of RB row blocks: half u / RB, row block u % RB; rows at `at`.
+  template <int RB>
+  __device__ __forceinline__ i32x4 row_fragment(uint32_t at, int u) const {
+    return *reinterpret_cast<const i32x4*>(lds + ((at + a_read) ^ (u / RB * 64)) + u % RB * (WM * 16 * kStage));
+  }
+  __device__ __forceinline__ void read_matrix(uint32_t slot, int h, int j) {
+    bf[h][j] = *reinterpret_cast<const i32x4*>(lds + ((slot * kBBytes + b_read) ^ (h * 64)) + j * (16 * kStage));
+  }
+
+  // An epoch, from one barrier to the next, issues the loads of the rows of stage `s` and of the
+  // matrix of stage s + 1: the first three loads of rows in the three slots after the barrier, the
+  // others over the next stage's 2 RB - 3 slots before its barrier.  Place of load j of those.
+  template <int RB>
+  static constexpr int late_slot(int j, int n) { return j * (2 * RB - kAhead) / n; }
+
+  // Stage s; its matrix in slot `now`, those of the next two in `next` and `last`; kPar: which half
+  // of the ring holds its first row fragments.  kFast: all row blocks in use, and every load of a
+  // whole stage.
+  template <int RB, bool kFast, int kPar>
+  __device__ __forceinline__ void stage(int s, uint32_t now, uint32_t next, uint32_t last) {
+    constexpr int kSlots = 2 * RB, kTurn = kSlots - kAhead, kFrom = kPar * kSlots % kRing;
+    constexpr int kRowLoads = kFast ? (RB * 2 * WM + kWaves - 1) / kWaves : kALoads;
+    constexpr int kLate = (kRowLoads > kAhead ? kRowLoads - kAhead : 0) + kBLoads;
+    const uint32_t at = (s & 1) * kABytes, at_next = kABytes - at;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      load_in_row(i, more2, s, after);
-      if (i == kTurn) {
-        // Stage s + 1 has landed, for every wave: only the loads of stage s + 2 may be on their way.
-        if (!more2) wait_loads<0>();
-        else if (turn == 0) wait_loads<issued(kTurn, 0)>();
-        else wait_loads<issued(kTurn, 1)>();
-        lds_barrier<15>();
+    for (int u = 0; u < kSlots; ++u) {
+      if (u == kTurn) {
+        // The rows of stage s + 1 have landed (the youngest loads are of the matrix of stage s + 2,
+        // all others older), and this wave has read all it needs of stage s.
+        if (kFast || s + 2 < stages) wait_loads<kBLoads>();
+        else wait_loads<0>();
+        lds_barrier();
       }
-      const int f = i + 2;
-      af[(2 * kSet + f) % kRing] = f < TM ? row_fragment(now, f) : row_fragment(next, f - TM);
-      if (i == kTurn) {
+      if (u >= kTurn) {
+        const int i = u - kTurn;
+        if (i < kRowLoads && (kFast || (i < a_loads && s + 2 < stages))) load_rows<kFast>(s + 2, i);
+      } else {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) read_matrix<1 - kSet>((s + 1) & 1, j);
+        for (int j = 0; j < kLate; ++j) {
+          if (late_slot<RB>(j, kLate) != u) continue;
+          const int i = j - (kLate - kBLoads);  // of the matrix, or of the rows from the fourth on
+          if (i >= 0) {
+            if (kFast || s + 2 < stages) load_matrix<kFast>(s + 2, last, i);
+          } else if (kFast || (kAhead + j < a_loads && s + 1 < stages)) {
+            load_rows<kFast>(s + 1, kAhead + j);
+          }
+        }
       }
-      if (i < blocks) {
-        const Fragment& a = af[(2 * kSet + i) % kRing];
+      const int v = u + kAhead;
+      i32x4& ahead = af[(kFrom + v) % kRing];
+      if (v >= kSlots) ahead = row_fragment<RB>(at_next, v - kSlots);
+      else if (kFast || v % RB < blocks) ahead = row_fragment<RB>(at, v);
+      // The second half's columns, before they are used and before the barrier; the next stage's,
+      // after it and in the second half.
+      constexpr int kHalfFrom = RB > TN + 2 ? RB - TN - 2 : 0, kHalfTo = RB < kTurn ? RB - 1 : kTurn - 1;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        if (u == (kHalfFrom + j < kHalfTo ? kHalfFrom + j : kHalfTo)) read_matrix(now, 1, j);
+        if (u == (kTurn > RB ? kTurn : RB) + j / 2) read_matrix(next, 0, j);
+      }
+      if (kFast || u % RB < blocks) {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[kSet][j].lo, a.lo, acc[i][j], 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[kSet][j].hi, a.hi, acc[i][j], 0, 0, 0);
+          acc[u % RB][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[u / RB][j], af[(kFrom + u) % kRing],
+                                                                 acc[u % RB][j], 0, 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // Each SIMD has one of the first four waves and one of the others; the former load in the first
-  // half of the rows, the latter in the second.  A load holds its wave until the address unit has
-  // taken it, and only the other wave keeps the matrix unit busy then.  (Tiles of two row blocks
-  // a wave are for streaming the matrix: all load at once.)
-  static constexpr int kTurns = TM > 2 ? 2 : 1;
-  static constexpr int kHalf = TM / 2, kPieces = (kLoads + kHalf - 1) / kHalf;
-  static constexpr int issued(int row, int turn) {  // loads of a wave when it has been through `row`
-    const int n = (row + 1 - turn * kHalf) * kPieces;
-    return n < 0 ? 0 : n < kLoads ? n : kLoads;
-  }
-  __device__ __forceinline__ void load_in_row(int i, bool more2, int s, uint32_t slot) const {
-#pragma unroll
-    for (int n = 0; n < kPieces; ++n) {
-      const int j = i % kHalf * kPieces + n;
-      if (more2 && turn == i / kHalf && j < kLoads) load_piece(s + 2, slot, j);
+  static __device__ __forceinline__ uint32_t after(uint32_t slot) { return slot == kBSlots - 1 ? 0 : slot + 1; }
+  // Two stages at a time while all their loads are of whole stages.
+  template <int RB>
+  __device__ __forceinline__ void fast_stages(int& s, uint32_t& slot) {
+    for (; s + 3 < whole; s += 2) {
+      const uint32_t one = after(slot), two = after(one);
+      stage<RB, true, 0>(s, slot, one, two);
+      stage<RB, true, 1>(s + 1, one, two, slot);
+      slot = two;
     }
   }
 
@@ -187,25 +216,42 @@ struct Int8Gemm {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) load_piece(0, 0, j);
+    for (int i = 0; i < kBLoads; ++i) load_matrix<false>(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i)
+      if (i < a_loads) load_rows<false>(0, i);
     if (stages > 1) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) load_piece(1, 1, j);
+      for (int i = 0; i < kBLoads; ++i) load_matrix<false>(1, 1, i);
+      wait_loads<kBLoads>();
+    } else {
+      wait_loads<0>();
     }
-    if (stages > 1) wait_loads<kLoads>();
-    else wait_loads<0>();
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) read_matrix<0>(0, j);
-    af[0] = row_fragment(0, 0);
-    af[1] = row_fragment(0, 1);
-    // (past the last stage, fragments are read from a slot that nobody uses)
-    uint32_t slot = 0;
-    for (int s = 0; s < stages; s += 2) {
-      const uint32_t one = slot == 2 ? 0 : slot + 1, two = one == 2 ? 0 : one + 1;
-      step<0>(s, slot, one, two);
-      if (s + 1 < stages) step<1>(s + 1, one, two, slot);
-      slot = two;
+    for (int i = 0; i < kAhead && i < kALoads; ++i)
+      if (i < a_loads && stages > 1) load_rows<false>(1, i);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) af[u] = row_fragment<TM>(0, u);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) read_matrix(0, 0, j);
+    int s = 0;
+    uint32_t slot = 0;  // of the matrix of stage s
+    if constexpr (TM == 8) {
+      if (blocks == 8) fast_stages<8>(s, slot);
+      else if (blocks == 7) fast_stages<7>(s, slot);
+      else if (blocks == 6) fast_stages<6>(s, slot);
+      else if (blocks == 5) fast_stages<5>(s, slot);
+      else if (blocks == 4) fast_stages<4>(s, slot);
+      else if (blocks == 3) fast_stages<3>(s, slot);
+    }
+    // The last stages, and tiles of fewer rows.  (Past the last stage, fragments are read from a
+    // slot that nobody uses.)
+#pragma unroll 1
+    for (; s < stages; ++s) {
+      const uint32_t one = after(slot);
+      stage<TM, false, 0>(s, slot, one, after(one));
+      slot = one;
     }
   }
 
@@ -262,7 +308,7 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const int64_t groups = r.wanted > r.E ? r.E : r.wanted, rows = (r.wanted + r.E - 1) / r.E;
   const int64_t columns = (int64_t)g.out_cols * (kGlu ? 2 : 1);
   const bool small = rows <= 32 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
-  return small ? launch<kGlu, 2, 2, 2, 4>(g, stream) : launch<kGlu, 6, 4, 2, 4>(g, stream);
+  return small ? launch<kGlu, 2, 2, 2, 4>(g, stream) : launch<kGlu, 8, 4, 2, 4>(g, stream);
 }
 
 }  // namespace
