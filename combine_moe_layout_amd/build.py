@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libep.so")
 SOURCES = ["ep_api.hip", "ep_layout.hip", "ep_dispatch.hip", "ep_fused.hip", "ep_combine.hip",
            "ep_group.hip", "ep_scales.hip", "ep_aux.hip", "ep_gemm_tile.hip", "ep_gemm_fp8.hip",
-           "ep_gemm_few.hip", "ep_gemm_int8.hip", "ep_int8.hip", "ep_grad.hip", "ep_route.hip", "ep_norm.hip"]
+           "ep_gemm_few.hip", "ep_gemm_int8.hip", "ep_gemm_int8_few.hip", "ep_int8.hip", "ep_grad.hip", "ep_route.hip", "ep_norm.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

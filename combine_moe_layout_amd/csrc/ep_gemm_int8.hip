@@ -18,11 +18,13 @@
 // matrix operand of stage s + 3 that of stage s.  So the matrix, which may come from HBM, is on
 // its way for two stages.
 //
-// The stages of a tile are code without a branch, made for each number of row blocks from 3 to 8:
+// The stages of a tile are code without a branch, made for each number of row blocks from 2 to 8:
 // two waves share a matrix unit, and one hides what the other does besides only as long as that is
 // shorter than four matrix instructions.  Branches around the row blocks and loads made the
 // product of 8192^3 470 us; without them it takes 393 (2.8 POP/s; the same matrix instructions
 // alone, without loads and LDS reads, 300).
+#include <math.h>
+
 #include "ep_int8.h"
 
 namespace ep {
@@ -150,7 +152,7 @@ struct Int8Gemm {
   template <int RB, bool kFast, int kPar>
   __device__ __forceinline__ void stage(int s, uint32_t now, uint32_t next, uint32_t last) {
     constexpr int kSlots = 2 * RB, kTurn = kSlots - kAhead, kFrom = kPar * kSlots % kRing;
-    constexpr int kRowLoads = kFast ? (RB * 2 * WM + kWaves - 1) / kWaves : kALoads;
+    constexpr int kRowLoads = (RB * 2 * WM + kWaves - 1) / kWaves;
     constexpr int kLate = (kRowLoads > kAhead ? kRowLoads - kAhead : 0) + kBLoads;
     const uint32_t at = (s & 1) * kABytes, at_next = kABytes - at;
 #pragma unroll
@@ -202,7 +204,8 @@ struct Int8Gemm {
   // Two stages at a time while all their loads are of whole stages.
   template <int RB>
   __device__ __forceinline__ void fast_stages(int& s, uint32_t& slot) {
-    for (; s + 3 < whole; s += 2) {
+    if constexpr (RB > TM) return;
+    else for (; s + 3 < whole; s += 2) {
       const uint32_t one = after(slot), two = after(one);
       stage<RB, true, 0>(s, slot, one, two);
       stage<RB, true, 1>(s + 1, one, two, slot);
@@ -232,32 +235,45 @@ struct Int8Gemm {
     for (int i = 0; i < kAhead && i < kALoads; ++i)
       if (i < a_loads && stages > 1) load_rows<false>(1, i);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) af[u] = row_fragment<TM>(0, u);
-#pragma unroll
     for (int j = 0; j < TN; ++j) read_matrix(0, 0, j);
     int s = 0;
     uint32_t slot = 0;  // of the matrix of stage s
-    if constexpr (TM == 8) {
+    if (TM == 2 || blocks <= 2) {
+      first_rows<2>();
+      fast_stages<2>(s, slot);
+      last_stages<2>(s, slot);
+    } else {
+      first_rows<TM>();
       if (blocks == 8) fast_stages<8>(s, slot);
       else if (blocks == 7) fast_stages<7>(s, slot);
       else if (blocks == 6) fast_stages<6>(s, slot);
       else if (blocks == 5) fast_stages<5>(s, slot);
       else if (blocks == 4) fast_stages<4>(s, slot);
-      else if (blocks == 3) fast_stages<3>(s, slot);
+      else fast_stages<3>(s, slot);
+      last_stages<TM>(s, slot);
     }
-    // The last stages, and tiles of fewer rows.  (Past the last stage, fragments are read from a
-    // slot that nobody uses.)
+  }
+  template <int RB>
+  __device__ __forceinline__ void first_rows() {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) af[u] = row_fragment<RB>(0, u);
+  }
+  // The last three or four.  (Past the last stage, fragments are read from a slot that nobody uses.)
+  template <int RB>
+  __device__ __forceinline__ void last_stages(int s, uint32_t slot) {
+    s = __builtin_amdgcn_readfirstlane(s);  // (uniform, which the compiler loses sight of)
+    slot = __builtin_amdgcn_readfirstlane(slot);
 #pragma unroll 1
     for (; s < stages; ++s) {
       const uint32_t one = after(slot);
-      stage<TM, false, 0>(s, slot, one, after(one));
+      stage<RB, false, 0>(s, slot, one, after(one));
       slot = one;
     }
   }
 
-  __device__ __forceinline__ void run() {
+  __device__ __forceinline__ void run(int32_t height) {
     const int32_t ct = (g.out_cols + kOutCols - 1) / kOutCols;
-    if (!find_tile<4>(g.groups, kRows, ct, blockIdx.x, t)) return;
+    if (!find_tile<4>(g.groups, height, ct, blockIdx.x, t)) return;
     setup();
     accumulate();
     lds_barrier();
@@ -280,35 +296,74 @@ struct Int8Gemm {
   }
 };
 
+// height: rows of a tile, at most kRows.
 template <bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g) {
+__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
-  gemm.run();
+  gemm.run(height);
 }
 
 template <bool kGlu, int TM, int TN, int WM, int WN>
-hipError_t launch(const GemmArgs& g, hipStream_t stream) {
+hipError_t launch(const GemmArgs& g, int32_t height, hipStream_t stream) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   const int64_t ct = (g.out_cols + G::kOutCols - 1) / G::kOutCols;
-  const int64_t blocks = (max_row_tiles(g.groups, G::kRows) * ct + kXcds - 1) / kXcds * kXcds;
+  const int64_t blocks = (max_row_tiles(g.groups, height) * ct + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g);
+  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height);
   return hipGetLastError();
 }
 
-// Tiles of 64 x 128, two workgroups to a CU, where the big ones would leave the GPU waiting:
-// experts of few rows, whose products read the matrix and little else, and products with so few
-// tiles that all of the small ones run at once.
+// Estimated time of a product in tiles of `height` rows, in units of the 6.5 us that one row block
+// to a wave takes with 7168 channels.  A big tile of RB row blocks takes RB + 2 (39 us for 128 rows,
+// 52 for 192, 65 for 256), and a CU holds one; a small one takes 3.2 by itself and 6.5 where two
+// share a CU.  Few tiles run in rounds, the last of which may leave CUs idle; many even out.
+// Groups' rows scatter about their mean by its root, so that a mean just below the height makes
+// two tiles of every other group.
+// Measured, us, 128 / 192 / 256 rows: 7168 x 4096 channels and columns, 1024 rows 40 / 52 / 65, 3000
+// rows 87 / 68 / 72, 4096 rows 104 / 130 / 86; 8 experts of 256 rows, 2048 x 4096, 39 / 25 / 30.
+double estimate(int64_t groups, int64_t rows, int64_t columns, int32_t height) {
+  const int64_t column_tiles = (columns + (height > 64 ? 255 : 127)) / (height > 64 ? 256 : 128);
+  const double spread = groups > 1 ? sqrt((double)rows) : 0.0;
+  double count = 0, work = 0, longest = 0;
+  for (int k = -1; k <= 1; ++k) {
+    const int64_t here = (int64_t)((double)rows + k * spread);
+    const int64_t n = (here + height - 1) / height;
+    if (n <= 0) continue;
+    const int64_t each = (here + n - 1) / n, blocks = (each + 31) / 32;
+    const double cost = height > 64 ? (double)(blocks + 2) : 3.25;
+    count += (double)n / 3;
+    work += (double)n * cost / 3;
+    longest = cost > longest ? cost : longest;
+  }
+  const double tiles = (double)(groups * column_tiles) * count;
+  if (height == 64) return 3.2 + (tiles > kChipCUs ? 3.3 * (tiles - kChipCUs) / kChipCUs : 0.0);
+  if (tiles > 3 * kChipCUs) return (double)(groups * column_tiles) * work / kChipCUs;
+  return ceil(tiles / kChipCUs) * longest;
+}
+
+// Products whose 16 x 16 (of more rows: 32 x 16, 64 x 16) or 64 x 64 tiles all have a CU of their own
+// go to the kernel whose waves share out the reduction: 7168 channels, 4096 columns, us, that one /
+// small / big tiles: 1 row 8.4 / 20 / 29, 64 rows 11.6 / 20 / 29, 256 rows 24 / 22 / 39.  Experts of
+// at most 32 rows are bound by reading their matrices, which small tiles do faster (256 experts of
+// 512 x 2048, 32 rows each: 49 us against 55).
 template <bool kGlu>
 hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const RowGroups& r = g.groups;
   const int64_t groups = r.wanted > r.E ? r.E : r.wanted, rows = (r.wanted + r.E - 1) / r.E;
   const int64_t columns = (int64_t)g.out_cols * (kGlu ? 2 : 1);
-  const bool small = rows <= 32 || groups * ((rows + 63) / 64) * ((columns + 127) / 128) <= 2 * kChipCUs;
-  return small ? launch<kGlu, 2, 2, 2, 4>(g, stream) : launch<kGlu, 8, 4, 2, 4>(g, stream);
+  const auto tiles = [&](int64_t height, int64_t width) {
+    return groups * ((rows + height - 1) / height) * ((columns + width - 1) / width);
+  };
+  if (tiles(rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 16) <= kChipCUs) return launch_gemm_int8_few(g, rows, false, stream);
+  if (tiles(64, 64) <= kChipCUs) return launch_gemm_int8_few(g, rows, true, stream);
+  int32_t height = 64;
+  if (rows > 32)
+    for (int32_t h = 128; h <= 256; h += 64)
+      if (estimate(groups, rows, columns, h) <= estimate(groups, rows, columns, height)) height = h;
+  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, stream) : launch<kGlu, 8, 4, 2, 4>(g, height, stream);
 }
 
 }  // namespace
