@@ -226,7 +226,7 @@ int check_router(const ep_router_t* r, int64_t tokens, int32_t dtype, ep::RouteA
       tokens > kInt32Limit / k)
     return EP_ERR_SHAPE;
   *a = ep::RouteArgs{E, k, G, r->topk_groups, r->group_top, r->score == EP_SCORE_SOFTMAX,
-                     r->renormalize != 0, r->scale, 0, 0};
+                     r->renormalize != 0, r->scale, -1, 0};
   return EP_OK;
 }
 

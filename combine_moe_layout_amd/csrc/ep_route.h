@@ -14,7 +14,7 @@ struct RouteArgs {
   int32_t softmax;      // scores: softmax, else sigmoid
   int32_t renormalize;
   float scale;
-  int32_t group_lanes;  // set by the launcher: lanes of a group, 0 where groups are not whole lanes
+  int32_t group_shift;  // set by the launcher: a group is 2^group_shift whole lanes, or -1: not so
   int32_t shared;       // set by the launcher: bytes of LDS of one token for the groups
 };
 

@@ -13,13 +13,20 @@
 // the token's lanes by DPP moves on order-preserving integers, and the lowest lane that has it
 // (lanes are in the experts' order) owns it: the tie goes to the lower index by itself.
 //
-// The order is that of the keys as real numbers.  Logits are compared as they are; keys with
-// scores in them are made in fp32 first, and where two that the result depends on are closer
-// than fp32 can tell, the wave makes its tokens' keys again in fp64 (for random logits and
-// biases about one token in 300 at 256 experts).
+// The order is that of the keys as real numbers.  Logits are compared as they are.  Keys with
+// scores in them are made in fp32 first; choices go on past the k-th while the next might belong
+// before it, and where two candidates are closer than fp32 can tell (for random logits and biases
+// at 256 experts one token in 1000), the candidates' keys alone are made again in fp64.  Where that is
+// not enough -- groups too close to tell, more candidates than lanes -- the wave does all of
+// it in fp64.
 //
 // Weights over the chosen are taken relative to the largest one, so that they are right also
 // where every chosen score underflows.
+//
+// Bound by the rounds of choosing: a dozen vector instructions of maximum, ballot and removal each,
+// with lanes' keys sorted by fours beforehand.  8192 tokens, 256 experts, top-8, fp32: 6.9 us by
+// logits, 10.1 with a bias (14.1 with every near pair redone in fp64 as a whole token), 12.2 with
+// groups too; the reading takes 1.8.  65,536 tokens, 64 experts, top-6: 9.0 us, gradient 8.3.
 #include "ep_route.h"
 
 namespace ep {
@@ -59,39 +66,36 @@ __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
 __device__ __forceinline__ float usable(float l) {
   return l > -INFINITY ? fminf(l, kMostF32) : -INFINITY;  // (a comparison with NaN is false)
 }
-// Experts first .. first + V - 1 of token t; -inf past the last.  `whole`: E is a multiple of V.
+// Experts first .. first + V - 1 of token t; -inf past the last.  `fours`: E is a multiple of 4.
 template <int kType, int V>
-__device__ __forceinline__ void load_logits(const void* p, int64_t t, int E, int first, bool whole, float (&l)[V]) {
+__device__ __forceinline__ void load_logits(const void* p, int64_t t, int E, int first, bool fours, float (&l)[V]) {
   const int64_t at = t * E + first;
-  if (whole) {
-    if (first < E) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    if (fours && first + i < E) {
       if constexpr (kType == EP_F32) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + i);
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + i);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) l[i + c] = v[c];
-        }
+        for (int c = 0; c < 4; ++c) l[i + c] = v[c];
       } else {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at + i);
-          l[i] = elem_low<kType == EP_F16>(v.x);
-          l[i + 1] = elem_high<kType == EP_F16>(v.x);
-          l[i + 2] = elem_low<kType == EP_F16>(v.y);
-          l[i + 3] = elem_high<kType == EP_F16>(v.y);
-        }
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at + i);
+        l[i] = elem_low<kType == EP_F16>(v.x);
+        l[i + 1] = elem_high<kType == EP_F16>(v.x);
+        l[i + 2] = elem_low<kType == EP_F16>(v.y);
+        l[i + 3] = elem_high<kType == EP_F16>(v.y);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = -INFINITY;
+      for (int c = 0; c < 4; ++c) l[i + c] = first + i + c < E ? logit_at<kType>(p, at + i + c) : -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = first + i < E ? logit_at<kType>(p, at + i) : -INFINITY;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) l[i] = usable(l[i]);
+}
+template <int V>
+__device__ __forceinline__ void load_bias(const float* p, int E, int first, float (&b)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = p[min(first + i, E - 1)];
 }
 
 struct Choice {
@@ -121,48 +125,130 @@ __device__ __forceinline__ void softmax_sums(const float (&l)[V], R& top, R& sum
   sum = s > 0 ? s : 1;
 }
 
-// The choice with keys of type R (float, or double where float cannot tell), into
-// `chosen`.  Returns whether two keys or group scores that decide are closer than float's
-// rounding (never with double): then `chosen` may be wrong.
+// 1 / (1 + exp(-l)), within 2^-22 of itself in float: the hardware's 2^x and reciprocal are each
+// within 2^-23, the sum within 2^-24, and the slope takes a quarter of what the exponential is off.
+__device__ __forceinline__ float score_sigmoid(float l) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l * -1.44269504088896341f));
+}
+__device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(-l)); }
+
+// Whether two float keys (sums of `n` of them) may be in the other order as real numbers.  A key is
+// a score, within 2^-22, and half a step of its sum with the bias; softmax scores have a sum over
+// all experts in common, whose terms and additions (22 at most) are off by up to 2^-19.2 of it.
+__device__ __forceinline__ bool near(const RouteArgs& a, float larger, float smaller, float n) {
+  return larger - smaller <= n * (a.softmax ? 0x1p-18f : 0x1p-21f) * (1.0f + fabsf(larger));
+}
+
+// A lane's keys in fours, each sorted (neighbours change places, so equal keys stay in the experts'
+// order): the best of a lane is the best of the fours' first.
+template <typename K, int V>
+struct LaneKeys {
+  K key[V];
+  uint32_t places[V / 4];  // where in its four each sorted key was, a byte each
+  __device__ __forceinline__ void prepare() {
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      int at[4] = {0, 1, 2, 3};
+#pragma unroll
+      for (int pass = 3; pass > 0; --pass)
+#pragma unroll
+        for (int i = 0; i < pass; ++i) {
+          const K x = key[q + i], y = key[q + i + 1];
+          const int p = at[i];
+          const bool swap = y > x;
+          key[q + i] = swap ? y : x;
+          key[q + i + 1] = swap ? x : y;
+          at[i] = swap ? at[i + 1] : p;
+          at[i + 1] = swap ? p : at[i + 1];
+        }
+      places[q / 4] = at[0] | at[1] << 8 | at[2] << 16 | at[3] << 24;
+    }
+  }
+  __device__ __forceinline__ K best() const {
+    K k = key[0];
+#pragma unroll
+    for (int q = 4; q < V; q += 4) k = key[q] > k ? key[q] : k;
+    return k;
+  }
+  // Takes the best key, `k`, out; returns its place in the lane.
+  __device__ __forceinline__ int take(K k, K none) {
+    int place = 0;
+    bool open = true;
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      const bool hit = V == 4 || (open && key[q] == k);
+      open = open && !hit;
+      place = hit ? q + (int)(places[q / 4] & 0xFF) : place;
+      places[q / 4] = hit ? places[q / 4] >> 8 : places[q / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) key[q + i] = !hit ? key[q + i] : i < 3 ? key[q + i + 1] : none;
+    }
+    return place;
+  }
+};
+
+// One round of choosing: the largest key of a token, and the lowest lane that has it.
+template <int L, typename K>
+__device__ __forceinline__ K best_of_token(K mine, bool& owner) {
+  const K all = reduce_max<L>(mine);
+  const uint64_t have = __builtin_amdgcn_ballot_w64(mine == all);
+  const int lane = threadIdx.x & 63;
+  if constexpr (L == 64) {
+    owner = lane == (int)__builtin_ctzll(have);
+  } else {  // lanes before this one in the token that have it too
+    const uint64_t before = ((1ull << lane) - 1) & (~0ull << (lane / L * L));
+    owner = mine == all && (have & before) == 0;
+  }
+  return all;
+}
+
+// The choice with keys of type R (float, or double where float cannot tell), into `chosen`.
+// Returns whether float cannot (then `chosen` may be wrong); `wide`: L doubles of the token.
 template <typename R, int L, int V>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], const float* bias,
-                                       int lane, R* shared, Choice* chosen) {
+__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], const float* bias, const float (&bv)[V], int lane,
+                                       R* shared, double* wide, int32_t* chosen) {
   using K = std::conditional_t<sizeof(R) == 4, int32_t, int64_t>;
   constexpr bool kFloat = sizeof(R) == 4;
   const R none = -INFINITY;
   const K none_key = order_of(none);
-  // Rounding: a score is within 2^-21 of itself (exp, sum, quotient: a few steps of 2^-24
-  // each), the bias adds half a step of the sum; twice that for a difference, and twice for a
-  // sum of two.
-  const auto near = [](R larger, R smaller, R factor) {
-    return larger - smaller <= factor * (R)0x1p-20 * (1 + fabs(larger));
-  };
   const int first = lane * V;
-  const bool grouped = a.topk_groups < a.groups;
+  const bool grouped = a.topk_groups < a.groups, exact = bias == nullptr;  // exact: by logits
+  LaneKeys<K, V> keys;
+  uint32_t keep = (1u << V) - 1;  // experts in groups that stay
+  bool unsure = false;
   R key[V];
-  bool scored = bias != nullptr || (grouped && a.group_top == 2);
+  const bool scored = !exact || (grouped && a.group_top == 2);
   if (scored) {
     R top = 0, sum = 1;
     if (a.softmax) softmax_sums<R, L, V>(l, top, sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const R s = a.softmax ? exp_of((R)l[i] - top) / sum : 1 / (1 + exp_of(-(R)l[i]));
-      R k = s;
-      if (bias != nullptr) k += (R)(first + i < a.E ? bias[first + i] : 0.0f);
+      R k = a.softmax ? exp_of((R)l[i] - top) / sum : score_sigmoid((R)l[i]);
+      if (!exact) k += (R)bv[i];
       key[i] = l[i] > -INFINITY && k > none ? k : none;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = l[i];
   }
-  bool close = false;
-  uint32_t keep = (1u << V) - 1;  // experts in groups that stay
   if (grouped) {
-    // A group's score: its largest key, or the sum of its two largest.
-    const int n = a.E / a.groups;
-    R* const score = shared;                 // [groups]
-    const bool in_lanes = a.group_lanes > 0;  // a group is a power of two of whole lanes
-    if (in_lanes) {
+    R* const score = shared;  // [groups]: the largest key, or the sum of the two largest
+    // Whether group g stays: fewer than topk_groups are ahead of it.  The last that stays looks
+    // how far the best of those that do not is behind it.
+    const auto stays = [&](int g, R mine) {
+      int ahead = 0;
+      R behind = none;
+      for (int o = 0; o < a.groups; ++o) {
+        const R other = score[o];
+        const bool better = other > mine || (other == mine && o < g);
+        ahead += better;
+        if (!better && o != g) behind = fmax(behind, other);
+      }
+      if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none)
+        unsure |= near(a, (float)mine, (float)behind, 2.0f);
+      return ahead < a.topk_groups;
+    };
+    if (a.group_shift >= 0) {  // a group is 2^group_shift whole lanes
       R one = key[0], two = none;
 #pragma unroll
       for (int i = 1; i < V; ++i) {
@@ -176,24 +262,27 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         one = fmax(a1, b1);
         two = fmax(fmin(a1, b1), fmax(a2, b2));
       };
-      if (a.group_lanes > 1) merge(std::integral_constant<int, 0>());
-      if (a.group_lanes > 2) merge(std::integral_constant<int, 1>());
-      if (a.group_lanes > 4) merge(std::integral_constant<int, 2>());
-      if (a.group_lanes > 8) merge(std::integral_constant<int, 3>());
-      if (a.group_lanes > 16) merge(std::integral_constant<int, 4>());
+      if (a.group_shift > 0) merge(std::integral_constant<int, 0>());
+      if (a.group_shift > 1) merge(std::integral_constant<int, 1>());
+      if (a.group_shift > 2) merge(std::integral_constant<int, 2>());
+      if (a.group_shift > 3) merge(std::integral_constant<int, 3>());
+      if (a.group_shift > 4) merge(std::integral_constant<int, 4>());
       if (a.group_top == 2 && two > none) one += two;
-      if (lane % a.group_lanes == 0 && first < a.E) score[first / n] = one;
+      const int g = lane >> a.group_shift;
+      if (g < a.groups && lane == g << a.group_shift) score[g] = one;
       wave_lds_fence();
+      if (!stays(g, one)) keep = 0;
     } else {
-      R* const keys = shared + a.groups;
+      const int n = a.E / a.groups;
+      R* const all = shared + a.groups;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (first + i < a.E) keys[first + i] = key[i];
+        if (first + i < a.E) all[first + i] = key[i];
       wave_lds_fence();
       for (int g = lane; g < a.groups; g += L) {
         R one = none, two = none;
         for (int i = 0; i < n; ++i) {
-          const R k = keys[g * n + i];
+          const R k = all[g * n + i];
           two = fmax(two, fmin(one, k));
           one = fmax(one, k);
         }
@@ -201,67 +290,80 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         score[g] = one;
       }
       wave_lds_fence();
-    }
-    // A group stays if fewer than topk_groups are ahead of it.  The last that stays looks how
-    // far the best of those that do not is behind it.
-    int last_group = -1;
-    bool stays = false;
+      int group = -1;
+      bool stay = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int g = min(first + i, a.E - 1) / n;
-      if (g != last_group) {
-        last_group = g;
-        const R mine = score[g];
-        int ahead = 0;
-        R behind = none;
-        for (int o = 0; o < a.groups; ++o) {
-          const R other = score[o];
-          const bool better = other > mine || (other == mine && o < g);
-          ahead += better;
-          if (!better && o != g) behind = fmax(behind, other);
+      for (int i = 0; i < V; ++i) {
+        const int g = min(first + i, a.E - 1) / n;
+        if (g != group) {
+          group = g;
+          stay = stays(g, score[g]);
         }
-        stays = ahead < a.topk_groups;
-        if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none) close |= near(mine, behind, 2);
+        if (!stay) keep &= ~(1u << i);
       }
-      if (!stays) keep &= ~(1u << i);
     }
     wave_lds_fence();
   }
-  const bool exact = bias == nullptr;  // by logits
-  K order[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) order[i] = keep >> i & 1 ? order_of(exact ? (R)l[i] : key[i]) : none_key;
-  K before = none_key;
-  // One more than k, to see how far behind the first that is not chosen is.
-  const int rounds = kFloat && !exact ? a.k + 1 : a.k;
-  for (int j = 0; j < rounds; ++j) {
-    K best = order[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) best = order[i] > best ? order[i] : best;
-    const K all = reduce_max<L>(best);
-    if (kFloat && !exact && j > 0 && all > none_key) close |= near(value_of(before), value_of(all), 1);
-    before = all;
-    const uint64_t have = __builtin_amdgcn_ballot_w64(best == all);
-    const int seg = (threadIdx.x & 63) / L * L;
-    const uint64_t mine = have >> seg & (~0ull >> (64 - L));
-    if (lane == __builtin_ctzll(mine)) {
-      int e = -1;
-      float le = -INFINITY;
-      bool open = true;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool hit = open && order[i] == all;
-        if (hit) {
-          e = first + i;
-          le = l[i];
-          order[i] = none_key;
-          open = false;
-        }
-      }
-      if (j < a.k) chosen[j] = all > none_key ? Choice{e, le} : Choice{-1, -INFINITY};
+  for (int i = 0; i < V; ++i) keys.key[i] = keep >> i & 1 ? order_of(exact ? (R)l[i] : key[i]) : none_key;
+  keys.prepare();
+  bool owner;
+  if (!kFloat || exact) {
+    for (int j = 0; j < a.k; ++j) {
+      const K all = best_of_token<L>(keys.best(), owner);
+      if (owner) chosen[j] = all > none_key ? first + keys.take(all, none_key) : -1;
     }
+    return unsure;
   }
-  return close;
+  // The k largest, and those after them that may belong before the k-th as real numbers.
+  K kept = none_key, last = none_key;  // of choice `lane`, of choice k - 1
+  int count = a.k;
+  for (int j = 0;; ++j) {
+    const K all = best_of_token<L>(keys.best(), owner);
+    if (j >= a.k) {
+      const bool more = all > none_key && near(a, (float)value_of(last), (float)value_of(all), 1.0f);
+      if (__builtin_amdgcn_ballot_w64(more) == 0) break;
+      if (j >= L) {  // (L choices at most)
+        unsure |= more;
+        break;
+      }
+      if (!more) owner = false;
+      count = more ? j + 1 : count;
+    } else {
+      last = all;
+    }
+    if (owner) chosen[j] = all > none_key ? first + keys.take(all, none_key) : -1;
+    if (lane == j) kept = all;
+  }
+  const K before = (K)__shfl_up((int)kept, 1);
+  const bool close = lane > 0 && lane < count && kept > none_key &&
+                     near(a, (float)value_of(before), (float)value_of(kept), 1.0f);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(close) == 0, 1)) return unsure;
+  // Again in fp64, for the candidates alone: a lane takes one and finds its place.
+  double top = 0, sum = 1;
+  if (a.softmax) softmax_sums<double, L, V>(l, top, sum);
+  wave_lds_fence();
+  const int e = lane < count ? chosen[lane] : -1;
+  const int from = max(e, 0) / V;  // its logit is in that lane of the token, at place e % V
+  float le = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float v = __shfl(l[i], from, L);
+    le = max(e, 0) % V == i ? v : le;
+  }
+  double k = -INFINITY;
+  if (e >= 0) k = (a.softmax ? exp((double)le - top) / sum : score_sigmoid((double)le)) + (double)bias[e];
+  wide[lane] = k;
+  wave_lds_fence();
+  int place = 0;
+  for (int i = 0; i < count; ++i) {
+    const double other = wide[i];
+    const int id = chosen[i];
+    place += id >= 0 && (other > k || (other == k && id < e));
+  }
+  wave_lds_fence();
+  if (e >= 0 && place < a.k) chosen[place] = e;  // (missing choices are behind all others already)
+  return unsure;
 }
 
 // The weights' shares over the chosen, in lane j for choice j (0 past the last):
@@ -287,20 +389,26 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const void* __restrict_
                                                          const float* __restrict__ bias, int64_t tokens,
                                                          RouteArgs a, int64_t* __restrict__ idx,
                                                          float* __restrict__ weights) {
-  __shared__ Choice choices[kThreads];                    // k <= L of each token
+  __shared__ int32_t choices[kThreads];                   // up to L of each token
+  __shared__ double wide[kThreads];
   extern __shared__ __align__(16) double group_memory[];  // a.shared bytes of each token
   const int lane = threadIdx.x % L, local = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x / L) + local;
   const int64_t from = t < tokens ? t : tokens - 1;  // (every lane takes part in every exchange)
+  float bv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bv[i] = 0.0f;
+  if (bias != nullptr) load_bias<V>(bias, a.E, lane * V, bv);
   float l[V];
-  load_logits<kType, V>(logits, from, a.E, lane * V, a.E % V == 0, l);
-  Choice* const chosen = choices + local * L;
+  load_logits<kType, V>(logits, from, a.E, lane * V, a.E % 4 == 0, l);
+  int32_t* const chosen = choices + local * L;
   char* const shared = reinterpret_cast<char*>(group_memory) + local * a.shared;
-  const bool close = choose<float, L, V>(a, l, bias, lane, reinterpret_cast<float*>(shared), chosen);
-  if (__builtin_amdgcn_ballot_w64(close) != 0)
-    choose<double, L, V>(a, l, bias, lane, reinterpret_cast<double*>(shared), chosen);
+  const bool unsure = choose<float, L, V>(a, l, bias, bv, lane, reinterpret_cast<float*>(shared), wide + local * L, chosen);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(unsure) != 0, 0))
+    choose<double, L, V>(a, l, bias, bv, lane, reinterpret_cast<double*>(shared), wide + local * L, chosen);
   wave_lds_fence();
-  const Choice c = lane < a.k ? chosen[lane] : Choice{-1, -INFINITY};
+  Choice c = {lane < a.k ? chosen[lane] : -1, -INFINITY};
+  if (c.expert >= 0) c.logit = usable(logit_at<kType>(logits, from * a.E + c.expert));
   float w;
   if (a.renormalize) {
     w = share_of<L>(a, c);
@@ -322,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const void* __restrict_
 //   renormalised   g_j = scale u_j sum_i u_i (dw_j - dw_i)     (sigmoid: times 1 - s_j)
 //   softmax        g_j = scale u_j dw_j, and every expert gets -p_e sum_i g_i
 //   sigmoid        g_j = scale u_j dw_j (1 - s_j)
-// scattered to the experts' places in the order of j, so ids that come twice add up.  The
+// brought to the experts' places through LDS; an id that comes twice has its sum in order.  The
 // sum of differences keeps its digits where one choice has nearly all the weight.
 // --------------------------------------------------------------------------
 template <int kType, int L, int V>
@@ -332,6 +440,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(const float* __res
                                                               RouteArgs a, void* __restrict__ dlogits) {
   constexpr int kTokens = kThreads / L;
   __shared__ float2 pairs[kThreads];  // (share, dw), then (expert, gradient)
+  __shared__ __align__(16) float rows[kThreads * V];
   const int lane = threadIdx.x % L, local = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * kTokens + local;
   const int64_t from = t < tokens ? t : tokens - 1;
@@ -347,7 +456,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(const float* __res
   }
   float l[V];
   const bool dense = a.softmax && !a.renormalize;
-  if (dense) load_logits<kType, V>(logits, from, a.E, lane * V, a.E % V == 0, l);
+  if (dense) load_logits<kType, V>(logits, from, a.E, lane * V, a.E % 4 == 0, l);
   float g, top = 0.0f, sum = 1.0f, mean = 0.0f;
   if (a.renormalize) {
     const float u = share_of<L>(a, c);
@@ -365,38 +474,48 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(const float* __res
     g = dw * sigmoid_of(c.logit) * a.scale;
   }
   if (!a.softmax) g = c.logit > -INFINITY ? g / (1.0f + expf(c.logit)) : 0.0f;
+  // The sum of an expert's entries, by the first of them, to the expert's place.
+  float* const row = rows + local * (L * V);
+#pragma unroll
+  for (int i = 0; i < V; i += 4) *reinterpret_cast<f32x4*>(row + lane * V + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   mine[lane] = float2{__int_as_float(c.expert), g};
   wave_lds_fence();
-  float d[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) d[i] = dense ? -(expf(l[i] - top) / sum) * mean : 0.0f;
-  const int first = lane * V;
+  float total = 0.0f;
+  bool first_entry = c.expert >= 0;
   for (int j = 0; j < a.k; ++j) {
     const float2 p = mine[j];
-    const int at = __float_as_int(p.x) - first;
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] += at == i ? p.y : 0.0f;
+    const bool same = __float_as_int(p.x) == c.expert;
+    total += same ? p.y : 0.0f;
+    first_entry = first_entry && !(same && j < lane);
   }
-  if (t >= tokens) return;
+  if (first_entry) row[c.expert] = total;
+  wave_lds_fence();
+  const int first = lane * V;
   const int64_t to = t * a.E + first;
-  if (a.E % V == 0) {
-    if (first >= a.E) return;
+  if (t >= tokens) return;
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
+  for (int i = 0; i < V; i += 4) {
+    f32x4 d = *reinterpret_cast<const f32x4*>(row + first + i);
+    if (dense) {
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) d[c4] -= expf(l[i + c4] - top) / sum * mean;
+    }
+    if (first + i >= a.E) continue;
+    if (a.E % 4 == 0) {
       if constexpr (kType == EP_F32) {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(dlogits) + to + i) = f32x4{d[i], d[i + 1], d[i + 2], d[i + 3]};
+        *reinterpret_cast<f32x4*>(static_cast<float*>(dlogits) + to + i) = d;
       } else {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dlogits) + to + i) =
-            uint2{elem_rne2<kType == EP_F16>(d[i], d[i + 1]), elem_rne2<kType == EP_F16>(d[i + 2], d[i + 3])};
+            uint2{elem_rne2<kType == EP_F16>(d[0], d[1]), elem_rne2<kType == EP_F16>(d[2], d[3])};
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (first + i < a.E) {
-        if constexpr (kType == EP_F32) static_cast<float*>(dlogits)[to + i] = d[i];
-        else static_cast<uint16_t*>(dlogits)[to + i] = elem_rne<kType == EP_F16>(d[i]);
-      }
+      for (int c4 = 0; c4 < 4; ++c4)
+        if (first + i + c4 < a.E) {
+          if constexpr (kType == EP_F32) static_cast<float*>(dlogits)[to + i + c4] = d[c4];
+          else static_cast<uint16_t*>(dlogits)[to + i + c4] = elem_rne<kType == EP_F16>(d[c4]);
+        }
+    }
   }
 }
 
@@ -441,8 +560,8 @@ hipError_t launch_route(const void* logits, const float* bias, int64_t tokens, R
   if (a.topk_groups < a.groups) {
     // Groups of whole lanes, a power of two of them, meet by lane exchanges; others in LDS.
     const int n = a.E / a.groups, lanes = n / s.experts;
-    if (n % s.experts == 0 && (lanes & (lanes - 1)) == 0) a.group_lanes = lanes;
-    a.shared = (a.groups + (a.group_lanes > 0 ? 0 : a.E)) * (int32_t)sizeof(double);
+    if (n % s.experts == 0 && (lanes & (lanes - 1)) == 0) a.group_shift = __builtin_ctz(lanes);
+    a.shared = (a.groups + (a.group_shift >= 0 ? 0 : a.E)) * (int32_t)sizeof(double);
   }
   return by_type(a, dtype, [&](auto type, auto L, auto V) -> hipError_t {
     // (half a workgroup where a token's groups take 16 KiB)
