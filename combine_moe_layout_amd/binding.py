@@ -154,6 +154,8 @@ def _check(fn: str, status: int) -> None:
 
 # the current stream's handle of a device by number, without making a Stream object (2.7 us)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device's number, without a check of whether the GPU has been initialised
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
@@ -498,8 +500,11 @@ class _Call:
     def run(self, fn: str, stream, *args) -> None:
         """The entry point on the tensors' device, with the stream as its last argument."""
         f = getattr(lib(), fn)
-        if self.device == torch.cuda.current_device():
-            status = f(*args, _stream(stream))
+        if self.device == _device():
+            if stream is None and _raw_stream is not None:
+                status = f(*args, _raw_stream(self.device))
+            else:
+                status = f(*args, _stream(stream))
         else:
             with torch.cuda.device(self.device):
                 status = f(*args, _stream(stream))

@@ -13,7 +13,10 @@
 //
 // Bound by HBM, as FP8 dispatch: one read of x, a row write for each of the token's pairs.  A row
 // stays in its lanes' registers, 16 channels (two loads, one store of codes) to a vector, between
-// its maximum and its codes.
+// its maximum and its codes.  65536 rows of 2048: 71 us (5.6 TB/s); dispatch of 8192 x 7168 to 8
+// experts each: 97 us (6.0 TB/s).  Dispatch's stores go past the caches, those of rows where they
+// stand do not: written past them, 1024 x 7168 rows and the product that reads them take 58 us
+// together, 50 us as it is.
 #include "ep_int8.h"
 
 namespace ep {
@@ -94,9 +97,11 @@ __global__ __launch_bounds__(kMaxLanes) void int8_rows_kernel(const u32x4* __res
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = lane + i * lanes;
-    const u32x4 zero = {0, 0, 0, 0};
-    in[i][0] = v < vecs ? from[2 * v] : zero;
-    in[i][1] = v < vecs ? from[2 * v + 1] : zero;
+    in[i][0] = in[i][1] = u32x4{0, 0, 0, 0};
+    if (v < vecs) {
+      in[i][0] = from[2 * v];
+      in[i][1] = from[2 * v + 1];
+    }
   }
   uint32_t both = 0;
 #pragma unroll
@@ -147,11 +152,14 @@ template <bool kF16>
 hipError_t launch(const void* x, int64_t rows, int32_t hidden, int32_t k, const int32_t* slots,
                   const RowGroups& groups, void* codes, float* scales, hipStream_t stream) {
   const int vecs = hidden / 16;
-  int vectors = 1, lanes = (vecs + 63) / 64 * 64;
-  while (lanes > kMaxLanes) {
-    vectors *= 2;
-    lanes = ((vecs + vectors - 1) / vectors + 63) / 64 * 64;
-  }
+  // Rows where they stand: two vectors to a lane beyond one wave's 64 (8192 x 7168: 31.4 us, 37.6
+  // with one; four up to one wave's 256: 65536 x 2048 in 71.4, 74.0).  Dispatch: one as long as a
+  // workgroup holds the row, for its k stores to be spread wide (8192 tokens of 4096 to 6 experts:
+  // 41 us, 64 with four).
+  int vectors = 1;
+  if (slots == nullptr && vecs > 64) vectors = vecs > 128 && vecs <= 256 ? 4 : 2;
+  while ((vecs + vectors - 1) / vectors > kMaxLanes) vectors *= 2;
+  const int lanes = ((vecs + vectors - 1) / vectors + 63) / 64 * 64;
   const int here = lanes == 64 ? 4 : 1;
   const int64_t blocks = (rows + here - 1) / here;
   if (!grid_fits(blocks, lanes * here)) return hipErrorInvalidValue;

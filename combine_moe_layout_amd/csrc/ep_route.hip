@@ -134,7 +134,7 @@ __device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(
 
 // Whether two float keys (sums of `n` of them) may be in the other order as real numbers.  A key is
 // a score, within 2^-22, and half a step of its sum with the bias; softmax scores have a sum over
-// all experts in common, whose terms and additions (22 at most) are off by up to 2^-19.2 of it.
+// all experts in common, whose terms and additions (22 at most) are off by up to 2^-18.8 of it.
 __device__ __forceinline__ bool near(const RouteArgs& a, float larger, float smaller, float n) {
   return larger - smaller <= n * (a.softmax ? 0x1p-18f : 0x1p-21f) * (1.0f + fabsf(larger));
 }
