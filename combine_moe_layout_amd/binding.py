@@ -478,11 +478,11 @@ class _Call:
             raise ValueError("%s must be a GPU tensor on the call's device %d" % (name, self.device))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        n = t.numel()
+        n = t.nbytes
         if n == 0:
             return None
         p = t.data_ptr()
-        self.ranges.append((p, p + n * dtype.itemsize, name))
+        self.ranges.append((p, p + n, name))
         return p
 
     def output(self, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
