@@ -132,11 +132,23 @@ __device__ __forceinline__ float score_sigmoid(float l) {
 }
 __device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(-l)); }
 
-// Whether two float keys (sums of `n` of them) may be in the other order as real numbers.  A key is
-// a score, within 2^-22, and half a step of its sum with the bias; softmax scores have a sum over
-// all experts in common, whose terms and additions (22 at most) are off by up to 2^-18.8 of it.
+// Whether two float keys may be in the other order as real numbers.  A key is a score, within 2^-22,
+// and half a step of its sum with the bias; softmax scores have a sum over all experts in common,
+// whose terms and additions (22 at most) are off by up to 2^-18.8 of it.  Groups' sums of two, n = 3:
+// four scores, 2^-20, and the roundings of the keys and the sums, 2^-24 times (2 + 4 |sum|) for each
+// of the groups where neither key is below -(1 + |sum|) (see sum_of_two).
 __device__ __forceinline__ bool near(const RouteArgs& a, float larger, float smaller, float n) {
   return larger - smaller <= n * (a.softmax ? 0x1p-18f : 0x1p-21f) * (1.0f + fabsf(larger));
+}
+
+// A group's score of its two largest keys.  Where the second is so negative that the keys' roundings
+// are more than `near` allows a sum, float cannot tell.
+template <typename R>
+__device__ __forceinline__ R sum_of_two(R one, R two, bool& unsure) {
+  if (!(two > -INFINITY)) return one;
+  const R sum = one + two;
+  if (sizeof(R) == 4 && -two > 1 + fabs(sum)) unsure = true;
+  return sum;
 }
 
 // A lane's keys in fours, each sorted (neighbours change places, so equal keys stay in the experts'
@@ -245,7 +257,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         if (!better && o != g) behind = fmax(behind, other);
       }
       if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none)
-        unsure |= near(a, (float)mine, (float)behind, 2.0f);
+        unsure |= near(a, (float)mine, (float)behind, a.group_top == 2 ? 3.0f : 1.0f);
       return ahead < a.topk_groups;
     };
     if (a.group_shift >= 0) {  // a group is 2^group_shift whole lanes
@@ -267,7 +279,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
       if (a.group_shift > 2) merge(std::integral_constant<int, 2>());
       if (a.group_shift > 3) merge(std::integral_constant<int, 3>());
       if (a.group_shift > 4) merge(std::integral_constant<int, 4>());
-      if (a.group_top == 2 && two > none) one += two;
+      if (a.group_top == 2) one = sum_of_two(one, two, unsure);
       const int g = lane >> a.group_shift;
       if (g < a.groups && lane == g << a.group_shift) score[g] = one;
       wave_lds_fence();
@@ -286,7 +298,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
           two = fmax(two, fmin(one, k));
           one = fmax(one, k);
         }
-        if (a.group_top == 2 && two > none) one += two;
+        if (a.group_top == 2) one = sum_of_two(one, two, unsure);
         score[g] = one;
       }
       wave_lds_fence();

@@ -432,8 +432,8 @@ int ep_combine_groups(const void* z, const ep_layout_t* group_layout, int32_t hi
  * type, what the gradients need.  Rows that no pair uses are neither read nor
  * written, as with ep_dispatch, in the contiguous and the padded layout.
  * in_features and out_features: 8 to EP_MAX_HIDDEN and multiples of 8, with
- * an FP8 dtype of 128; with EP_INT8 in_features a multiple of 16.  Pointers 16-byte aligned (scales 4).  out and preact
- * must not overlap the inputs.
+ * an FP8 dtype of 128; with EP_INT8 in_features a multiple of 16.  Pointers
+ * 16-byte aligned (scales 4).  out and preact must not overlap the inputs.
  * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
  */
 int ep_expert_gemm(const void* x, const void* x_scales, const void* weights,

@@ -241,6 +241,24 @@ def test_nonfinite_rows_stay_apart():
     assert torch.isnan(out[3]).all() and torch.isinf(out[5, 1]) and (out[7] == 0).all() and (normed[7] == 0).all()
 
 
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 elements: the last rows come out as by themselves."""
+    rows, H = 70_000, 65_536
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    last = torch.randn((3, H), device="cuda", generator=g).bfloat16()
+    w = torch.randn(H, device="cuda", generator=g).bfloat16()
+    y = torch.ones((rows, H), dtype=torch.bfloat16, device="cuda")
+    y[-3:] = last
+    out, few = torch.empty_like(y), torch.empty_like(last)
+    B.ep_block_norm(y, None, out, 0, EPS, post_weight=w)
+    B.ep_block_norm(last, None, few, 0, EPS, post_weight=w)
+    assert torch.equal(out[-3:], few)
+    B.ep_block_norm_grad(y, None, y, None, 0, None, EPS, post_weight=w, d_y=out)
+    B.ep_block_norm_grad(last, None, last, None, 0, None, EPS, post_weight=w, d_y=few)
+    assert torch.equal(out[-3:], few)
+
+
 def test_no_rows():
     e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     B.ep_block_norm(e, None, torch.empty_like(e), 0)

@@ -245,6 +245,34 @@ def test_nan_rows_give_nan_results():
     assert bad.nonzero().flatten().tolist() == [7, 20] and torch.isfinite(out[~bad]).all()
 
 
+def test_offsets_past_32_bits():
+    """Rows, results and matrices of more than 2^32 bytes: the last of them come out as by themselves."""
+    rows, K, N = 70_000, 65_536, 64
+    x = torch.ones((rows, K), dtype=BF, device="cuda")
+    x[-5:] = torch.randn((5, K), device="cuda", generator=gen(1)).to(BF)
+    q, s = torch.empty((rows, K), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    few_q, few_s = torch.empty_like(q[:5]), torch.empty_like(s[:5])
+    B.ep_quantize_int8(x, q, s, 0)
+    B.ep_quantize_int8(x[-5:].clone(), few_q, few_s, 0)
+    assert torch.equal(q[-5:], few_q) and torch.equal(s[-5:], few_s)
+    del x
+    w, ws = few_q[:1].expand(N, K).contiguous(), torch.rand(N, device="cuda", generator=gen(3))
+    out, few = torch.empty((rows, N), dtype=BF, device="cuda"), torch.empty((5, N), dtype=BF, device="cuda")
+    B.ep_linear_int8(q, s, w, ws, out)
+    B.ep_linear_int8(few_q, few_s, w, ws, few)
+    assert torch.equal(out[-5:], few)
+    # the rows' codes as a matrix of 70,000 columns, gates and ups 2.3e9 bytes apart
+    W, rs = 35_000, torch.rand(70_000, device="cuda", generator=gen(4))
+    for T in (3, 300):
+        a, sa = q[-5:].repeat(T, 1)[:T], torch.rand(T, device="cuda", generator=gen(5))
+        out, z = torch.empty((T, W), dtype=BF, device="cuda"), torch.empty((T, 2 * W), dtype=BF, device="cuda")
+        few, few_z = torch.empty((T, 8), dtype=BF, device="cuda"), torch.empty((T, 16), dtype=BF, device="cuda")
+        B.ep_linear_int8(a, sa, q, rs, out, act=B.EP_ACT_SWIGLU, preact=z)
+        B.ep_linear_int8(a, sa, torch.cat([q[W - 8:W], q[-8:]]), torch.cat([rs[W - 8:W], rs[-8:]]), few,
+                         act=B.EP_ACT_SWIGLU, preact=few_z)
+        assert torch.equal(z[:, W - 8:W], few_z[:, :8]) and torch.equal(z[:, -8:], few_z[:, 8:])
+
+
 def test_no_rows():
     e = lambda *s, dt=BF: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
     i8, f32 = torch.int8, torch.float32

@@ -106,6 +106,36 @@ def test_keys_closer_than_fp32_can_tell(E, groups, topk_groups, group_top, score
         check_weights(many, idx, w, score, True, 1.0)
 
 
+@pytest.mark.parametrize("E,groups,topk_groups", [(32, 8, 3), (64, 4, 2), (24, 8, 3), (600, 5, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_keys_that_cancel(E, groups, topk_groups, score):
+    """A group's two largest keys are large and of opposite signs: what fp32 rounds off of each is more
+    than the groups' sums, which are those of the scores alone, differ by."""
+    n, T = E // groups, 500
+    logits = torch.randn((T, E), device="cuda", generator=gen(E))
+    bias = torch.full((groups, n), -90000.0, device="cuda")
+    bias[:, 0], bias[:, 1] = 30000.0, -30000.0
+    router = B.EpRouter(E, 2, SCORES[score], groups, topk_groups, 2)
+    idx, w = route(logits, "fp32", router, bias.view(-1))
+    assert torch.equal(idx, ref.choice(logits, bias.view(-1), 2, score, groups, topk_groups, 2))
+    check_weights(logits, idx, w, score, True, 1.0)
+
+
+@pytest.mark.parametrize("E,groups,topk_groups,group_top", [(64, 1, 1, 1), (256, 8, 3, 2), (250, 5, 2, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases(E, groups, topk_groups, group_top, score):
+    """Experts with a bias of +inf come first, in their order; those with -inf never."""
+    logits = torch.randn((40, E), device="cuda", generator=gen(E))
+    bias = 0.1 * torch.randn(E, device="cuda", generator=gen(E + 1))
+    bias[torch.tensor([5, E - 3, E // 2])] = math.inf
+    bias[::4] = -math.inf
+    bias[7] = 3e38
+    router = B.EpRouter(E, 8, SCORES[score], groups, topk_groups, group_top)
+    idx, w = route(logits, "fp32", router, bias)
+    assert torch.equal(idx, ref.choice(logits, bias, 8, score, groups, topk_groups, group_top))
+    check_weights(logits, idx, w, score, True, 1.0)
+
+
 @pytest.mark.parametrize("E,k,groups,topk_groups", [(8, 3, 1, 1), (64, 6, 1, 1), (256, 8, 8, 4), (100, 8, 5, 2), (600, 16, 1, 1)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
@@ -261,6 +291,21 @@ def test_many_tokens():
     key, order = torch.sort(logits.double(), dim=1, descending=True, stable=True)
     assert torch.equal(idx, order[:, :k])
     check_weights(logits, idx, w, "sigmoid", True, 1.0)
+
+
+def test_offsets_past_32_bits():
+    """More logits than 2^31: the last tokens come out as by themselves, forward and gradient."""
+    T, E, k = 2_100_000, 1024, 2
+    logits = torch.zeros((T, E), device="cuda", dtype=torch.bfloat16)
+    logits[-9:] = torch.randn((9, E), device="cuda", generator=gen(3)).bfloat16()
+    router = B.EpRouter(E, k, B.EP_SCORE_SOFTMAX, 8, 4, 1, False)
+    idx, w = route(logits, "bf16", router)
+    few, few_w = route(logits[-9:].clone(), "bf16", router)
+    assert torch.equal(idx[-9:], few) and torch.equal(w[-9:], few_w) and (idx[:-9] == torch.arange(k, device="cuda")).all()
+    d, few_d = torch.empty_like(logits), torch.empty_like(logits[-9:])
+    B.ep_route_grad(w, logits, idx, router, d, B.EP_BF16)
+    B.ep_route_grad(few_w, logits[-9:].clone(), few, router, few_d, B.EP_BF16)
+    assert torch.equal(d[-9:], few_d)
 
 
 def test_no_tokens():
