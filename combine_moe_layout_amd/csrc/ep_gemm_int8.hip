@@ -5,11 +5,11 @@
 // The sum is exact: at most 65,536 products of magnitude at most 2^14 in 32 bits.  It is rounded
 // to fp32 once, and the scales, bias, activation and residual follow in fp32.
 //
-// A workgroup of 8 waves makes a tile of 256 rows and 256 columns, 128 x 64 to a wave (64 x 128,
-// 32 x 32 to a wave, where that is too much for the rows there are).  A stage is 128 channels,
-// walked as two halves of 64 (the matrix instruction's reduction): a wave holds its columns'
-// fragments of one half, and goes through its row blocks with three of theirs read ahead, so
-// that 128 sums and all fragments fit 220 registers.  (Fragments of whole stages, twice, spilled;
+// A workgroup of 8 waves makes a tile of up to 128, 192 or 256 rows and 256 columns, 128 x 64 to a
+// wave (64 x 128, 32 x 32 to a wave, where that is too much for the rows there are).  A stage is 128
+// channels, walked as two halves of 64 (the matrix instruction's reduction): a wave holds its
+// columns' fragments of one half, and goes through its row blocks with three of theirs read ahead,
+// so that 128 sums and all fragments fit 241 registers.  (Fragments of whole stages, twice, spilled;
 // a spilled register's reload waits for the loads to LDS as well.)
 //
 // LDS holds two stages of rows and three of the matrix operand, all 160 KiB of it.  There is one
@@ -21,8 +21,10 @@
 // The stages of a tile are code without a branch, made for each number of row blocks from 2 to 8:
 // two waves share a matrix unit, and one hides what the other does besides only as long as that is
 // shorter than four matrix instructions.  Branches around the row blocks and loads made the
-// product of 8192^3 470 us; without them it takes 393 (2.8 POP/s; the same matrix instructions
-// alone, without loads and LDS reads, 300).
+// product of 8192^3 470 us; without them it takes 384 (2.9 POP/s; the same matrix instructions
+// alone, without loads and LDS reads, 300).  65,536 rows of 7168 channels to 4096 columns: 1470 us
+// (2.6 POP/s) for 16 matrices, 1830 for 256 of as many rows each (7.5 GB of them, 4.1 TB/s), 2250
+// where experts have 256 rows on average (1.7 POP/s): those with more make two tiles.
 #include <math.h>
 
 #include "ep_int8.h"
@@ -271,9 +273,11 @@ struct Int8Gemm {
     }
   }
 
-  __device__ __forceinline__ void run(int32_t height) {
+  __device__ __forceinline__ void run(int32_t height, bool single) {
     const int32_t ct = (g.out_cols + kOutCols - 1) / kOutCols;
-    if (!find_tile<4>(g.groups, height, ct, blockIdx.x, t)) return;
+    if (!(single ? find_tile<1>(g.groups, height, ct, blockIdx.x, t)
+                 : find_tile<4>(g.groups, height, ct, blockIdx.x, t)))
+      return;
     setup();
     accumulate();
     lds_barrier();
@@ -296,23 +300,24 @@ struct Int8Gemm {
   }
 };
 
-// height: rows of a tile, at most kRows.
+// height: rows of a tile, at most kRows.  single: a row tile's columns follow one another, instead of
+// four row tiles' at each column.
 template <bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height) {
+__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height, bool single) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
-  gemm.run(height);
+  gemm.run(height, single);
 }
 
 template <bool kGlu, int TM, int TN, int WM, int WN>
-hipError_t launch(const GemmArgs& g, int32_t height, hipStream_t stream) {
+hipError_t launch(const GemmArgs& g, int32_t height, bool single, hipStream_t stream) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   const int64_t ct = (g.out_cols + G::kOutCols - 1) / G::kOutCols;
   const int64_t blocks = (max_row_tiles(g.groups, height) * ct + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height);
+  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height, single);
   return hipGetLastError();
 }
 
@@ -363,7 +368,12 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   if (rows > 32)
     for (int32_t h = 128; h <= 256; h += 64)
       if (estimate(groups, rows, columns, h) <= estimate(groups, rows, columns, height)) height = h;
-  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, stream) : launch<kGlu, 8, 4, 2, 4>(g, height, stream);
+  // Groups of about one row tile have no matrix to share between row tiles: a row tile's columns share
+  // its rows (256 experts of about 256 rows, 7168 x 4096: 2357 us, 2482 in fours; all groups of 256
+  // rows: 1921, 1986).  8192^3 takes 408 in fours, 435 one by one.
+  const bool single = groups > 1 && rows <= height;
+  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, single, stream)
+                      : launch<kGlu, 8, 4, 2, 4>(g, height, single, stream);
 }
 
 }  // namespace
