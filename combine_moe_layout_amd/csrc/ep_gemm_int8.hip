@@ -12,6 +12,11 @@
 // so that 128 sums and all fragments fit 241 registers.  (Fragments of whole stages, twice, spilled;
 // a spilled register's reload waits for the loads to LDS as well.)
 //
+// What bounds a stage of a short tile is LDS: of 128 bytes a cycle, a stage's fragments take 128 RB +
+// 512 cycles and its loads 32 RB + 256, the matrix instructions 256 RB (RB row blocks to a wave), so
+// that short tiles cost what RB + 2 row blocks would.  Four waves of 128 x 128 read a third less, but
+// with one wave to a SIMD nothing hides its waits: 8192^3 in 440 us.
+//
 // LDS holds two stages of rows and three of the matrix operand, all 160 KiB of it.  There is one
 // barrier to a stage, three slots before its end, where its last rows have been read and the next
 // stage has landed: after it the rows of stage s + 2 take the place of those of stage s, and the
@@ -23,8 +28,8 @@
 // shorter than four matrix instructions.  Branches around the row blocks and loads made the
 // product of 8192^3 470 us; without them it takes 384 (2.9 POP/s; the same matrix instructions
 // alone, without loads and LDS reads, 300).  65,536 rows of 7168 channels to 4096 columns: 1470 us
-// (2.6 POP/s) for 16 matrices, 1830 for 256 of as many rows each (7.5 GB of them, 4.1 TB/s), 2250
-// where experts have 256 rows on average (1.7 POP/s): those with more make two tiles.
+// (2.6 POP/s) for 16 matrices, 1830 for 256 of 256 rows each (7.5 GB of matrices, 4.1 TB/s), 2140
+// where experts have 256 rows on average (1.8 POP/s): those with more make two tiles.
 #include <math.h>
 
 #include "ep_int8.h"
@@ -273,9 +278,9 @@ struct Int8Gemm {
     }
   }
 
-  __device__ __forceinline__ void run(int32_t height, bool single) {
+  __device__ __forceinline__ void run(int32_t height, bool by_group) {
     const int32_t ct = (g.out_cols + kOutCols - 1) / kOutCols;
-    if (!(single ? find_tile<1>(g.groups, height, ct, blockIdx.x, t)
+    if (!(by_group ? find_tile<0>(g.groups, height, ct, blockIdx.x, t)
                  : find_tile<4>(g.groups, height, ct, blockIdx.x, t)))
       return;
     setup();
@@ -300,24 +305,24 @@ struct Int8Gemm {
   }
 };
 
-// height: rows of a tile, at most kRows.  single: a row tile's columns follow one another, instead of
-// four row tiles' at each column.
+// height: rows of a tile, at most kRows.  by_group: a group's row tiles walk the columns together,
+// instead of four row tiles of any groups.
 template <bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height, bool single) {
+__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height, bool by_group) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
-  gemm.run(height, single);
+  gemm.run(height, by_group);
 }
 
 template <bool kGlu, int TM, int TN, int WM, int WN>
-hipError_t launch(const GemmArgs& g, int32_t height, bool single, hipStream_t stream) {
+hipError_t launch(const GemmArgs& g, int32_t height, bool by_group, hipStream_t stream) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   const int64_t ct = (g.out_cols + G::kOutCols - 1) / G::kOutCols;
   const int64_t blocks = (max_row_tiles(g.groups, height) * ct + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height, single);
+  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height, by_group);
   return hipGetLastError();
 }
 
@@ -368,12 +373,14 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   if (rows > 32)
     for (int32_t h = 128; h <= 256; h += 64)
       if (estimate(groups, rows, columns, h) <= estimate(groups, rows, columns, height)) height = h;
-  // Groups of about one row tile have no matrix to share between row tiles: a row tile's columns share
-  // its rows (256 experts of about 256 rows, 7168 x 4096: 2357 us, 2482 in fours; all groups of 256
-  // rows: 1921, 1986).  8192^3 takes 408 in fours, 435 one by one.
-  const bool single = groups > 1 && rows <= height;
-  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, single, stream)
-                      : launch<kGlu, 8, 4, 2, 4>(g, height, single, stream);
+  // Groups of up to eight row tiles take them all through the columns together: what runs at one time
+  // on an XCD then shares rows, and the row tiles of a group a matrix panel, in its L2.  7168 x 4096, us,
+  // by groups / in fours: 256 experts of about 256 rows 2140 / 2400 (8.5 and 10.3 GB from beyond L2),
+  // of about 512 rows 3530 / 3850; 16 experts of about 2048 rows 775 / 805.  Of 8192 rows, 8 experts:
+  // 1814 / 1458.
+  const bool by_group = groups > 1 && rows <= 8 * height;
+  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, by_group, stream)
+                      : launch<kGlu, 8, 4, 2, 4>(g, height, by_group, stream);
 }
 
 }  // namespace
