@@ -94,8 +94,8 @@ struct Tile {
 // get false.  Workgroups go round robin to the 8 XCDs, so that each XCD takes
 // one contiguous eighth of the tiles; within it, bands of kBand row tiles walk
 // the columns together, so that what runs at one time on an XCD shares row
-// panels and (row tiles of one group) matrix panels in its L2.  kBand 0: a group's
-// row tiles walk the columns together, and no others.
+// panels and (row tiles of one group) matrix panels in its L2.  kOneGroup: bands
+// are of row tiles of one group.
 // A group's rows are shared out evenly among its row tiles, in steps of 16 (so
 // that 257 rows make tiles of 144 and 113 rows and not of 256 and 1; a kernel
 // skips a tile's blocks of 16 rows that it does not have).
@@ -105,7 +105,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {  // the same in every la
   return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(v >> 32)) << 32) |
                    (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)v));
 }
-template <int kBand>
+template <int kBand, bool kOneGroup = false>
 __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, int32_t col_tiles,
                                           uint32_t block, Tile& t) {
   const int lane = threadIdx.x & 63;
@@ -122,7 +122,7 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   const int64_t in_share = block / kXcds;
   const int64_t id = (int64_t)(block % kXcds) * share + in_share;
   if (in_share >= share || id >= total) return false;
-  constexpr int32_t kRows = kBand > 0 ? kBand : 1;
+  constexpr int32_t kRows = kOneGroup ? 1 : kBand;
   const int64_t band_tiles = (int64_t)kRows * col_tiles;
   const int32_t band = (int32_t)(id / band_tiles);
   const int32_t rem = (int32_t)(id - band * band_tiles);
@@ -145,10 +145,11 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int32_t height, in
   left = __builtin_amdgcn_readlane(left, owner);
   const int32_t count = group_count(g, t.e);
   const int32_t even = (tiles_of(count, tiles_of(count, height)) + 15) & ~15;
-  if constexpr (kBand == 0) {
-    const int32_t n = tiles_of(count, height), at = left * col_tiles + t.col;
-    t.col = at / n;
-    left = at - t.col * n;
+  if constexpr (kOneGroup) {
+    const int32_t n = tiles_of(count, height), at = left * col_tiles + t.col, whole = kBand * col_tiles;
+    const int32_t rest = at % whole, rows = min(kBand, n - at / whole * kBand);
+    left = at / whole * kBand + rest % rows;
+    t.col = rest / rows;
   }
   const int32_t each = min(height, even);
   t.rows = (int32_t)min((int64_t)each, count - (int64_t)left * each);

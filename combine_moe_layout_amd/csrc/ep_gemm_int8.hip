@@ -28,7 +28,7 @@
 // shorter than four matrix instructions.  Branches around the row blocks and loads made the
 // product of 8192^3 470 us; without them it takes 384 (2.9 POP/s; the same matrix instructions
 // alone, without loads and LDS reads, 300).  65,536 rows of 7168 channels to 4096 columns: 1470 us
-// (2.6 POP/s) for 16 matrices, 1830 for 256 of 256 rows each (7.5 GB of matrices, 4.1 TB/s), 2140
+// (2.6 POP/s) for 16 matrices, 1830 for 256 of 256 rows each (7.5 GB of matrices, 4.1 TB/s), 2130
 // where experts have 256 rows on average (1.8 POP/s): those with more make two tiles.
 #include <math.h>
 
@@ -278,11 +278,13 @@ struct Int8Gemm {
     }
   }
 
-  __device__ __forceinline__ void run(int32_t height, bool by_group) {
+  __device__ __forceinline__ void run(int32_t height) {
     const int32_t ct = (g.out_cols + kOutCols - 1) / kOutCols;
-    if (!(by_group ? find_tile<0>(g.groups, height, ct, blockIdx.x, t)
-                 : find_tile<4>(g.groups, height, ct, blockIdx.x, t)))
-      return;
+    // Bands of up to eight row tiles of one group: what runs at one time on an XCD then shares rows and
+    // matrix panels in its L2.  7168 x 4096, us, so / in fours of any groups: 256 experts of about 256
+    // rows 2130 / 2400 (8.5 and 10.3 GB from beyond L2), of about 512 rows 3540 / 3850, 16 experts of
+    // about 4096 rows 1537 / 1573; without a bound on the band, 8 experts of 8192 rows 1814 / 1458.
+    if (!find_tile<8, true>(g.groups, height, ct, blockIdx.x, t)) return;
     setup();
     accumulate();
     lds_barrier();
@@ -305,24 +307,23 @@ struct Int8Gemm {
   }
 };
 
-// height: rows of a tile, at most kRows.  by_group: a group's row tiles walk the columns together,
-// instead of four row tiles of any groups.
+// height: rows of a tile, at most kRows.
 template <bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height, bool by_group) {
+__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
-  gemm.run(height, by_group);
+  gemm.run(height);
 }
 
 template <bool kGlu, int TM, int TN, int WM, int WN>
-hipError_t launch(const GemmArgs& g, int32_t height, bool by_group, hipStream_t stream) {
+hipError_t launch(const GemmArgs& g, int32_t height, hipStream_t stream) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   const int64_t ct = (g.out_cols + G::kOutCols - 1) / G::kOutCols;
   const int64_t blocks = (max_row_tiles(g.groups, height) * ct + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, kWaves * 64)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
-  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height, by_group);
+  gemm_int8_kernel<kGlu, TM, TN, WM, WN><<<(uint32_t)blocks, kWaves * 64, 0, stream>>>(g, height);
   return hipGetLastError();
 }
 
@@ -373,14 +374,8 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   if (rows > 32)
     for (int32_t h = 128; h <= 256; h += 64)
       if (estimate(groups, rows, columns, h) <= estimate(groups, rows, columns, height)) height = h;
-  // Groups of up to eight row tiles take them all through the columns together: what runs at one time
-  // on an XCD then shares rows, and the row tiles of a group a matrix panel, in its L2.  7168 x 4096, us,
-  // by groups / in fours: 256 experts of about 256 rows 2140 / 2400 (8.5 and 10.3 GB from beyond L2),
-  // of about 512 rows 3530 / 3850; 16 experts of about 2048 rows 775 / 805.  Of 8192 rows, 8 experts:
-  // 1814 / 1458.
-  const bool by_group = groups > 1 && rows <= 8 * height;
-  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, by_group, stream)
-                      : launch<kGlu, 8, 4, 2, 4>(g, height, by_group, stream);
+  return height == 64 ? launch<kGlu, 2, 2, 2, 4>(g, 64, stream)
+                      : launch<kGlu, 8, 4, 2, 4>(g, height, stream);
 }
 
 }  // namespace
