@@ -18,7 +18,8 @@
 // fixed order, so the result does not depend on timing.  16,384 rows of 4096: 145 us (5.5 TB/s),
 // 344 us without the next row's loads in flight, 234 us with them but with the weights loaded for
 // each row, behind them.  More than 8192 channels leave no registers for that, and up to 16,384 the
-// sums are in LDS (2048 x 16,384: 126 us; 176 in registers, which spilled).
+// sums are in LDS (2048 x 16,384: 126 us; 176 in registers, which spilled; 300 by the wide rows'
+// kernel, which more channels go to).
 #include "ep_norm.h"
 
 namespace ep {
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
     else if (row + step < a.rows) load(now, row + step);
   }
   // The block's rows meet in LDS, in order, and its sums go to the workspace.
-  constexpr bool kSmall = V <= 2 && kPrefetch;
+  constexpr bool kSmall = kPrefetch;
   __shared__ float sums[kSmall ? kRowsPerBlock : 1][kSmall ? 64 * V * 8 : 1];
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -388,6 +389,151 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
         reinterpret_cast<f32x4*>(to)[2 * v] = f32x4{f[0], f[1], f[2], f[3]};
         reinterpret_cast<f32x4*>(to)[2 * v + 1] = f32x4{f[4], f[5], f[6], f[7]};
       }
+    }
+  }
+}
+
+// More than kLdsVecs * 8 channels: a row's vectors do not fit its lanes' registers (kept there, they
+// spilled: 2048 rows of 32,768 in 811 us, of 65,536 in 2777 us).  A workgroup goes over its row four
+// times, for y's sum of squares, x's sums, D and the outputs, and computes x and dx anew each time; the
+// row comes from the caches after the first (589 us, 1230 us; two workgroups to a CU no better).  Its sums of the weights' gradients are
+// kept in the workspace.
+template <bool kF16>
+__global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArgs a, int64_t partials) {
+  __shared__ float part[2][3][2 * kMaxWaves];
+  const int32_t vecs = a.hidden / 8, lanes = blockDim.x;
+  const u32x4* const post = static_cast<const u32x4*>(a.post_weight);
+  const u32x4* const pre = static_cast<const u32x4*>(a.pre_weight);
+  const bool has_y = a.y != nullptr, has_pre = a.d_normed != nullptr, has_post = post != nullptr;
+  const bool weights = a.d_post_weight != nullptr || a.d_pre_weight != nullptr;
+  const float mean = 1.0f / (float)a.hidden;
+  float* const own_post = a.d_post_weight != nullptr ? a.partial + (int64_t)blockIdx.x * a.hidden : nullptr;
+  float* const own_pre = a.d_pre_weight != nullptr ? a.partial + (partials + blockIdx.x) * a.hidden : nullptr;
+  const u32x4 zero = {0, 0, 0, 0};
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const bool first = row == blockIdx.x;
+    const int64_t at = row * vecs;
+    const auto vector = [&](const void* p, int v, float (&f)[8]) {
+      unpack8<kF16>(p != nullptr ? static_cast<const u32x4*>(p)[at + v] : zero, f);
+    };
+    const float gate = a.gate != nullptr ? a.gate[row] : 1.0f;
+    float s = 1.0f, r = 0.0f, back = 0.0f;
+    if (has_post) {
+      float squares[1] = {0.0f};
+#pragma unroll 4
+      for (int v = threadIdx.x; v < vecs; v += lanes) {
+        float f[8];
+        vector(a.y, v, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) squares[0] = fmaf(f[k], f[k], squares[0]);
+      }
+      row_sums(squares, lanes, part[turn][0]);
+      s = inverse_rms(squares[0], a.hidden, a.eps);
+    }
+    // x, and pre dn
+    const auto hidden = [&](int v, float (&x)[8], float (&d)[8]) {
+      float f[8], w[8];
+      vector(a.y, v, f);
+      vector(a.residual, v, x);
+      vector(a.d_normed, v, d);
+      if (has_post) {
+        unpack8<kF16>(post[v], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * s * w[k];
+      }
+      unpack8<kF16>(pre[v], w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = fmaf(gate, f[k], a.residual_scale * x[k]);
+        d[k] *= w[k];
+      }
+    };
+    if (has_pre) {
+      float sums[2] = {0.0f, 0.0f};  // x^2, pre dn x
+#pragma unroll 2
+      for (int v = threadIdx.x; v < vecs; v += lanes) {
+        float x[8], d[8];
+        hidden(v, x, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sums[0] = fmaf(x[k], x[k], sums[0]);
+          sums[1] = fmaf(d[k], x[k], sums[1]);
+        }
+      }
+      row_sums(sums, lanes, part[turn][1]);
+      r = inverse_rms(sums[0], a.hidden, a.eps);
+      back = r * r * r * (sums[1] * mean);
+    }
+    const auto gradient = [&](int v, float (&x)[8], float (&dx)[8]) {
+      vector(a.d_out, v, dx);
+      if (!has_pre) return;
+      float d[8];
+      hidden(v, x, d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dx[k] += fmaf(r, d[k], -x[k] * back);
+    };
+    const auto add = [&](float* own, int v, const float (&p)[8], const float (&q)[8]) {
+      f32x4* const to = reinterpret_cast<f32x4*>(own) + 2 * v;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (!first) sum = to[h];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = fmaf(p[4 * h + k], q[4 * h + k], sum[k]);
+        to[h] = sum;
+      }
+    };
+    float dot[1] = {0.0f};
+    if (weights || (has_y && (has_post || a.d_gate != nullptr))) {
+#pragma unroll 2
+      for (int v = threadIdx.x; v < vecs; v += lanes) {
+        float x[8], dx[8], f[8], w[8];
+        gradient(v, x, dx);
+        if (own_pre != nullptr) {
+          vector(a.d_normed, v, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] *= r;
+          add(own_pre, v, f, x);
+        }
+        vector(a.y, v, f);
+        if (has_post) {
+          if (own_post != nullptr) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = gate * s * f[k];
+            add(own_post, v, dx, x);
+          }
+          unpack8<kF16>(post[v], w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dx[k] *= w[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot[0] = fmaf(dx[k], f[k], dot[0]);
+      }
+      row_sums(dot, lanes, part[turn][2]);
+      if (a.d_gate != nullptr && threadIdx.x == 0) a.d_gate[row] = s * dot[0];
+    }
+    if (a.d_y == nullptr && a.d_residual == nullptr) continue;
+    const float along = gate * s, back_y = has_post ? gate * (s * s * s) * (dot[0] * mean) : 0.0f;
+#pragma unroll 2
+    for (int v = threadIdx.x; v < vecs; v += lanes) {
+      float x[8], dx[8], f[8], w[8];
+      gradient(v, x, dx);
+      vector(a.y, v, f);
+      if (a.d_residual != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = a.residual_scale * dx[k];
+        store_nt(static_cast<u32x4*>(a.d_residual) + at + v, pack8<kF16>(x));
+      }
+      if (a.d_y == nullptr) continue;
+      if (has_post) {
+        unpack8<kF16>(post[v], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dx[k] *= w[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = fmaf(along, dx[k], -f[k] * back_y);
+      store_nt(static_cast<u32x4*>(a.d_y) + at + v, pack8<kF16>(f));
     }
   }
 }
@@ -467,8 +613,7 @@ hipError_t gradient(const NormArgs& a, hipStream_t stream) {
     if (s.vectors == 1) run(block_norm_grad_kernel<kF16, 1, true>);
     else if (s.vectors == 2 && s.lanes <= kMaxLanes / 2) run(block_norm_grad_kernel<kF16, 2, true>);
     else if (s.vectors == 2) run(block_norm_grad_kernel<kF16, 2, false>);
-    else if (s.vectors == 4) run(block_norm_grad_kernel<kF16, 4, false>);
-    else run(block_norm_grad_kernel<kF16, 8, false>);
+    else block_norm_grad_wide_kernel<kF16><<<(uint32_t)blocks, threads, 0, stream>>>(a, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -212,6 +212,38 @@ def test_gradient_against_differences():
     assert abs(diff) > 30 and abs(diff - along) <= 4, (diff, along)
 
 
+@pytest.mark.parametrize("rows,H", [(600, 16_392), (515, 32_768)])
+def test_many_wide_rows(rows, H):
+    """Rows that no workgroup holds in registers, several to a workgroup: whole, in place, and with one
+    incoming gradient."""
+    print("[gpu-norm] wide", rows, H, flush=True)
+    for kind in KINDS:
+        v = inputs(rows, H, kind, torch.bfloat16)
+        want, size = exact_gradients(v, 0.75), sizes(v, 0.75)
+        got = gradients(v, 0, torch.bfloat16, 0.75, B.EP_GRAD_F32)
+        for k in got:
+            near(got[k], want[k], size[k], (kind, k))
+        again = gradients(v, 0, torch.bfloat16, 0.75, B.EP_GRAD_F32)
+        assert all(torch.equal(again[k], got[k]) for k in got)
+        for only in (("y",), ("pre",), ("gate", "post"), ("residual",)):
+            some = gradients(v, 0, torch.bfloat16, 0.75, B.EP_GRAD_F32, only=only) if any(v[k] is not None for k in only) else {}
+            assert all(torch.equal(some[k], got[k]) for k in some), only
+        if kind == "all":
+            a, b = v["d_out"].clone(), v["d_normed"].clone()
+            B.ep_block_norm_grad(a, b, v["y"], v["residual"], 0, None, EPS, v["post"], v["gate"], 0.75, v["pre"], d_y=a,
+                                 d_residual=b)
+            assert torch.equal(a, got["y"]) and torch.equal(b, got["residual"])
+            for gone in ("d_out", "d_normed"):
+                w = dict(v)
+                w[gone] = None
+                if gone == "d_normed":
+                    w["pre"] = None
+                want, size = exact_gradients(w, 1.0), sizes(w, 1.0)
+                got = gradients(w, 0, torch.bfloat16, 1.0)
+                for k in got:
+                    near(got[k], want[k], size[k], (gone, k))
+
+
 def test_outputs_in_place():
     for kind in ("all", "add"):
         v = inputs(33, 1000, kind, torch.bfloat16)
