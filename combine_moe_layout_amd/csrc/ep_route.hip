@@ -132,22 +132,27 @@ __device__ __forceinline__ float score_sigmoid(float l) {
 }
 __device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(-l)); }
 
-// Whether two float keys may be in the other order as real numbers.  A key is a score, within 2^-22,
-// and half a step of its sum with the bias; softmax scores have a sum over all experts in common,
-// whose terms and additions (22 at most) are off by up to 2^-18.8 of it.  Groups' sums of two, n = 3:
-// four scores, 2^-20, and the roundings of the keys and the sums, 2^-24 times (2 + 4 |sum|) for each
-// of the groups where neither key is below -(1 + |sum|) (see sum_of_two).
-__device__ __forceinline__ bool near(const RouteArgs& a, float larger, float smaller, float n) {
-  return larger - smaller <= n * (a.softmax ? 0x1p-18f : 0x1p-21f) * (1.0f + fabsf(larger));
+// Whether two float keys may be in the other order as real numbers.  A key is a score and half a step,
+// 2^-24 of it, of its sum with the bias.  `unit` covers what two scores are off by: sigmoid scores
+// 2^-22 each; softmax scores 2^-18.8 of themselves (the terms and additions, 22 at most, of the sum over
+// all experts), two of which are at most 1 and at most twice the largest, 1 / sum.  Groups' scores of
+// two keys, n = 3: see sum_of_two.
+__device__ __forceinline__ bool near(float unit, float larger, float smaller, float n) {
+  return larger - smaller <= n * (unit + 0x1p-21f * fabsf(larger));
+}
+__device__ __forceinline__ float near_unit(const RouteArgs& a, float sum) {
+  return a.softmax ? 0x1p-18f * fminf(1.0f, 2.0f / sum) : 0x1p-21f;
 }
 
-// A group's score of its two largest keys.  Where the second is so negative that the keys' roundings
-// are more than `near` allows a sum, float cannot tell.
+// A group's score of its two largest keys.  Its roundings are 2^-24 (|one| + |two| + |sum|), at most
+// 2^-23 (|two| + |sum|).  Where -two is at most 2 |sum| + c, that is 2^-23 (3 |sum| + c) for each of
+// two groups, and `near` with n = 3 has room for it: 3 * 2^-21 |sum|, and of 3 units what four scores
+// leave (sigmoid 2^-21, so c = 1; softmax 1.8 units, so c = 2^22 units).  Otherwise float cannot tell.
 template <typename R>
-__device__ __forceinline__ R sum_of_two(R one, R two, bool& unsure) {
+__device__ __forceinline__ R sum_of_two(R one, R two, bool softmax, float unit, bool& unsure) {
   if (!(two > -INFINITY)) return one;
   const R sum = one + two;
-  if (sizeof(R) == 4 && -two > 1 + fabs(sum)) unsure = true;
+  if (sizeof(R) == 4 && -two > 2 * fabs(sum) + (softmax ? 0x1p22f * unit : 1.0f)) unsure = true;
   return sum;
 }
 
@@ -230,9 +235,11 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
   bool unsure = false;
   R key[V];
   const bool scored = !exact || (grouped && a.group_top == 2);
+  float unit = 0.0f;
   if (scored) {
     R top = 0, sum = 1;
     if (a.softmax) softmax_sums<R, L, V>(l, top, sum);
+    unit = near_unit(a, (float)sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       R k = a.softmax ? exp_of((R)l[i] - top) / sum : score_sigmoid((R)l[i]);
@@ -257,7 +264,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         if (!better && o != g) behind = fmax(behind, other);
       }
       if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none)
-        unsure |= near(a, (float)mine, (float)behind, a.group_top == 2 ? 3.0f : 1.0f);
+        unsure |= near(unit, (float)mine, (float)behind, a.group_top == 2 ? 3.0f : 1.0f);
       return ahead < a.topk_groups;
     };
     if (a.group_shift >= 0) {  // a group is 2^group_shift whole lanes
@@ -279,7 +286,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
       if (a.group_shift > 2) merge(std::integral_constant<int, 2>());
       if (a.group_shift > 3) merge(std::integral_constant<int, 3>());
       if (a.group_shift > 4) merge(std::integral_constant<int, 4>());
-      if (a.group_top == 2) one = sum_of_two(one, two, unsure);
+      if (a.group_top == 2) one = sum_of_two(one, two, a.softmax, unit, unsure);
       const int g = lane >> a.group_shift;
       if (g < a.groups && lane == g << a.group_shift) score[g] = one;
       wave_lds_fence();
@@ -298,7 +305,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
           two = fmax(two, fmin(one, k));
           one = fmax(one, k);
         }
-        if (a.group_top == 2) one = sum_of_two(one, two, unsure);
+        if (a.group_top == 2) one = sum_of_two(one, two, a.softmax, unit, unsure);
         score[g] = one;
       }
       wave_lds_fence();
@@ -333,7 +340,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
   for (int j = 0;; ++j) {
     const K all = best_of_token<L>(keys.best(), owner);
     if (j >= a.k) {
-      const bool more = all > none_key && near(a, (float)value_of(last), (float)value_of(all), 1.0f);
+      const bool more = all > none_key && near(unit, (float)value_of(last), (float)value_of(all), 1.0f);
       if (__builtin_amdgcn_ballot_w64(more) == 0) break;
       if (j >= L) {  // (L choices at most)
         unsure |= more;
@@ -349,7 +356,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
   }
   const K before = (K)__shfl_up((int)kept, 1);
   const bool close = lane > 0 && lane < count && kept > none_key &&
-                     near(a, (float)value_of(before), (float)value_of(kept), 1.0f);
+                     near(unit, (float)value_of(before), (float)value_of(kept), 1.0f);
   if (__builtin_expect(__builtin_amdgcn_ballot_w64(close) == 0, 1)) return unsure;
   // Again in fp64, for the candidates alone: a lane takes one and finds its place.
   double top = 0, sum = 1;
