@@ -532,6 +532,7 @@ int ep_combine_grad(const void* dout, const void* expert_out, const float* topk_
  * layout: NULL, or a filled layout, whose receive rows x are (rows =
  * num_recv_rows): rows that no pair uses are then neither read nor written.
  * n: 16 to EP_MAX_HIDDEN, a multiple of 16.  x and q 16-byte aligned, not overlapping.
+ * A row takes 64 to 1024 threads; 2^32 threads or more are EP_ERR_LAUNCH.
  * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
  */
 int ep_quantize_int8(const void* x, const ep_layout_t* layout, int64_t rows, int32_t n,
@@ -578,7 +579,8 @@ typedef struct ep_router {
  * logits [T, E] of dtype EP_F32, EP_BF16 or EP_F16; bias fp32 [E] or NULL; topk_idx int64
  * and topk_weights fp32 [T, k].  Requires num_groups to divide E, k <= EP_MAX_TOPK and k <=
  * topk_groups * E / num_groups, group_top 2 only where groups have two experts, T * k below
- * 2^31.  logits 16-byte aligned.  Outputs must not overlap the inputs.
+ * 2^31.  logits 16-byte aligned.  Outputs must not overlap the inputs.  A token takes 8 to
+ * 64 threads; 2^32 threads or more are EP_ERR_LAUNCH.
  * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE (logits' type, score)
  * or EP_ERR_LAUNCH.
  */
@@ -608,7 +610,8 @@ int ep_route_grad(const float* d_topk_weights, const void* logits, const int64_t
  * be NULL, or pre_weight and normed together.  y, residual, out, normed [rows, hidden],
  * weights [hidden], of dtype EP_BF16 or EP_F16; gate fp32 [rows].  out or normed may be y or
  * residual itself.  eps > 0 and finite.  hidden: 8 to EP_MAX_HIDDEN, a multiple of 8; 0 <= rows
- * < 2^31.  Rows whose sum of squares leaves fp32's range are outside the definition.
+ * < 2^31.  Rows whose sum of squares leaves fp32's range are outside the definition.  A row
+ * takes 64 to 1024 threads; 2^32 threads or more are EP_ERR_LAUNCH (not in the gradient).
  * Returns EP_OK, EP_ERR_NULL, EP_ERR_SHAPE, EP_ERR_ALIGN, EP_ERR_DTYPE or EP_ERR_LAUNCH.
  */
 int ep_block_norm(const void* y, const void* post_weight, const float* gate, const void* residual,
