@@ -133,7 +133,7 @@ def library_path() -> str:
 
 def lib() -> ctypes.CDLL:
     """The loaded libep.so.  Raises if it has not been built."""
-    global _lib
+    global _lib, _devices
     if _lib is None:
         if not os.path.exists(_LIB_PATH):
             raise RuntimeError("libep.so is not built (%s); run `python -m "
@@ -143,7 +143,7 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
-        _lib = L
+        _lib, _devices = L, torch.cuda.device_count()
     return _lib
 
 
@@ -154,7 +154,9 @@ def _check(fn: str, status: int) -> None:
 
 # the current stream's handle of a device by number, without making a Stream object (2.7 us)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-# the current device's number, without a check of whether the GPU has been initialised
+# the current device's number, without a check of whether the GPU has been initialised, and how many
+# devices there are (set with the library: where there is one, it is the current one)
+_devices = 0
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -470,20 +472,22 @@ class _Call:
         """Device pointer (None stays None)."""
         if t is None:
             return None
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device or not t.is_contiguous():
+            self.refuse(t, name, dtype, shape)
+        p = t.data_ptr()
+        if p == 0:                  # no elements
+            return None
+        self.ranges.append((p, p + t.nbytes, name))
+        return p
+
+    def refuse(self, t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> None:
         if t.dtype is not dtype:
             raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
         if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
         if t.get_device() != self.device:
             raise ValueError("%s must be a GPU tensor on the call's device %d" % (name, self.device))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        n = t.nbytes
-        if n == 0:
-            return None
-        p = t.data_ptr()
-        self.ranges.append((p, p + n, name))
-        return p
+        raise ValueError("%s must be contiguous" % name)
 
     def output(self, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
                may_be: tuple = ()) -> int | None:
@@ -491,16 +495,18 @@ class _Call:
         (but may be one of those named in may_be, from its first element on)."""
         p = self.operand(t, name, dtype, shape)
         if p is not None:
-            mine = self.ranges[-1]
-            for lo, hi, other in self.ranges[:-1]:
-                if lo < mine[1] and p < hi and not (lo == p and other in may_be):
+            mine = self.ranges.pop()
+            end = mine[1]
+            for lo, hi, other in self.ranges:
+                if lo < end and p < hi and not (lo == p and other in may_be):
                     raise ValueError("%s overlaps %s" % (name, other))
+            self.ranges.append(mine)
         return p
 
     def run(self, fn: str, stream, *args) -> None:
         """The entry point on the tensors' device, with the stream as its last argument."""
         f = getattr(lib(), fn)
-        if self.device == _device():
+        if _devices == 1 or self.device == _device():
             if stream is None and _raw_stream is not None:
                 status = f(*args, _raw_stream(self.device))
             else:
