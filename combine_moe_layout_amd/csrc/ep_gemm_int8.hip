@@ -6,7 +6,7 @@
 // to fp32 once, and the scales, bias, activation and residual follow in fp32.
 //
 // A workgroup of 8 waves makes a tile of up to 128, 192 or 256 rows and 256 columns, 128 x 64 to a
-// wave (64 x 128, 32 x 32 to a wave, where that is too much for the rows there are).  A stage is 128
+// wave (128 x 128 or 64 x 128, 64 x 32 or 32 x 32 to a wave, where there are few).  A stage is 128
 // channels, walked as two halves of 64 (the matrix instruction's reduction): a wave holds its
 // columns' fragments of one half, and goes through its row blocks with three of theirs read ahead,
 // so that 128 sums and all fragments fit 241 registers.  (Fragments of whole stages, twice, spilled;
@@ -309,7 +309,7 @@ struct Int8Gemm {
 
 // height: rows of a tile, at most kRows.
 template <bool kGlu, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(kWaves * 64, TM > 2 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height) {
+__global__ __launch_bounds__(kWaves * 64, TM > 4 ? 2 : 4) void gemm_int8_kernel(GemmArgs g, int32_t height) {
   typedef Int8Gemm<kGlu, TM, TN, WM, WN> G;
   __shared__ __align__(1024) char lds[G::kLdsBytes];
   G gemm(g, lds);
@@ -370,6 +370,12 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   };
   if (tiles(rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 16) <= kChipCUs) return launch_gemm_int8_few(g, rows, false, stream);
   if (tiles(64, 64) <= kChipCUs) return launch_gemm_int8_few(g, rows, true, stream);
+  // Where 64 x 128 tiles would share CUs and 128 x 128 tiles do not, those: 7168 channels, 4096 columns,
+  // 640 rows 31 us (else 33), 1024 rows 34 (40); 4096 channels 20.5 (21.7), 22.5 (27.9); 2048 channels,
+  // 7168 columns, 300 rows 10.7 (12.2); 8 experts of 128 rows, 2048 x 4096, 21.6 (23.8).  Sharing CUs,
+  // they lose: 1280 rows of the first 46 (42).
+  if (rows > 32 && tiles(64, 128) > kChipCUs && tiles(128, 128) <= kChipCUs)
+    return launch<kGlu, 4, 2, 2, 4>(g, 128, stream);
   int32_t height = 64;
   if (rows > 32)
     for (int32_t h = 128; h <= 256; h += 64)

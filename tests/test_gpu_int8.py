@@ -219,6 +219,19 @@ def test_linear(T, K, N, name):
     check(out, act(z, name), act_error(z, off, name), "out alone")
 
 
+@pytest.mark.parametrize("T,K,N", [(640, 1040, 4096), (1000, 400, 4096), (705, 208, 4096), (4000, 144, 1008), (300, 2048, 7168)])
+@pytest.mark.parametrize("name", ["gelu", "swiglu"])
+def test_one_tile_for_each_cu(T, K, N, name):
+    """Sizes whose tiles of 128 x 128 number between half the CUs and all of them."""
+    test_linear(T, K, N // 2 if name == "swiglu" else N, name)
+
+
+@pytest.mark.parametrize("cap", [0, 150])
+def test_one_tile_for_each_cu_of_experts(cap):
+    test_experts(512, 2, 8, cap, 0.1, 336, 4096, "silu")
+    test_experts(512, 2, 8, cap, 0.1, 272, 2048, "swiglu")
+
+
 def test_largest_sums():
     """65,536 products of -128 and -128: 2^30, and its negative neighbours."""
     K = 65536
