@@ -355,11 +355,13 @@ double estimate(int64_t groups, int64_t rows, int64_t columns, int32_t height) {
   return ceil(tiles / kChipCUs) * longest;
 }
 
-// Products whose 16 x 16 (of more rows: 32 x 16, 64 x 16) or 64 x 64 tiles all have a CU of their own
-// go to the kernel whose waves share out the reduction: 7168 channels, 4096 columns, us, that one /
-// small / big tiles: 1 row 8.4 / 20 / 29, 64 rows 11.6 / 20 / 29, 256 rows 24 / 22 / 39.  Experts of
-// at most 32 rows are bound by reading their matrices, which small tiles do faster (256 experts of
-// 512 x 2048, 32 rows each: 49 us against 55).
+// Products whose tiles of 16, 32 or 64 rows and columns all have a CU of their own go to the kernel whose
+// waves share out the reduction, in the smallest such tiles: what a CU reads is what takes its time.
+// Matrices from HBM, 7168 channels, us: 16 rows, 8192 columns in 16 x 32 12.6, 64 x 32 14.8, 64 x 64
+// 21.3; 32 rows in 32 x 32 14.3, 64 x 64 22.1; 100 rows, 4096 columns in 64 x 32 16.2, 64 x 64 22.5.
+// 64 x 128 tiles of the kernel above instead: 1 row, 4096 columns 20 (7.7 in 16 x 16), 256 rows 30 (25
+// in 64 x 64).  Experts of at most 32 rows are bound by reading their matrices, which those tiles do
+// faster where there are many (256 experts of 512 x 2048, 32 rows each: 49 us against 55).
 template <bool kGlu>
 hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const RowGroups& r = g.groups;
@@ -368,8 +370,9 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const auto tiles = [&](int64_t height, int64_t width) {
     return groups * ((rows + height - 1) / height) * ((columns + width - 1) / width);
   };
-  if (tiles(rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 16) <= kChipCUs) return launch_gemm_int8_few(g, rows, false, stream);
-  if (tiles(64, 64) <= kChipCUs) return launch_gemm_int8_few(g, rows, true, stream);
+  const int32_t low = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  for (int32_t width = 16; width <= 64; width *= 2)
+    if (tiles(low, width) <= kChipCUs) return launch_gemm_int8_few(g, low, width, stream);
   // Where 64 x 128 tiles would share CUs and 128 x 128 tiles do not, those: 7168 channels, 4096 columns,
   // 640 rows 31 us (else 33), 1024 rows 34 (40); 4096 channels 20.5 (21.7), 22.5 (27.9); 2048 channels,
   // 7168 columns, 300 rows 10.7 (12.2); 8 experts of 128 rows, 2048 x 4096, 21.6 (23.8).  Sharing CUs,

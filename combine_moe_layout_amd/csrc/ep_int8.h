@@ -16,7 +16,7 @@ hipError_t launch_quantize_int8(const void* x, const RowGroups& groups, int32_t 
 
 // a, b: int8; a_scales [rows] and b_scales [E, columns of the product] fp32.
 hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t stream);
-// rows: about how many each group has.  wide: 64 x 64 tiles.
-hipError_t launch_gemm_int8_few(const GemmArgs& g, int64_t rows, bool wide, hipStream_t stream);
+// Tiles of 16, 32 or 64 rows and as many columns.
+hipError_t launch_gemm_int8_few(const GemmArgs& g, int32_t height, int32_t width, hipStream_t stream);
 
 }  // namespace ep

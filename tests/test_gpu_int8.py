@@ -232,6 +232,20 @@ def test_one_tile_for_each_cu_of_experts(cap):
     test_experts(512, 2, 8, cap, 0.1, 272, 2048, "swiglu")
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 1040, 8192), (16, 400, 16384), (20, 1040, 8192), (32, 272, 12000), (50, 2064, 6144),
+                                   (100, 400, 8192), (9, 16, 5008), (1, 16384, 4112)])
+@pytest.mark.parametrize("name", ["gelu", "swiglu"])
+def test_few_tiles(T, K, N, name):
+    """Every height and width of the tiles that share out the reduction, with a part of a chunk at its end."""
+    test_linear(T, K, N // 2 if name == "swiglu" else N, name)
+
+
+@pytest.mark.parametrize("T,N", [(30, 512), (30, 1024), (60, 1024), (60, 2000), (120, 1024)])
+def test_few_tiles_of_experts(T, N):
+    test_experts(T, 2, 4, 0, 0.1, 400, N, "none")
+    test_experts(T, 2, 4, 70, 0.0, 400, N // 2, "swiglu")
+
+
 def test_largest_sums():
     """65,536 products of -128 and -128: 2^30, and its negative neighbours."""
     K = 65536
