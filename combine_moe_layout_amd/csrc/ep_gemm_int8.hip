@@ -358,8 +358,8 @@ double estimate(int64_t groups, int64_t rows, int64_t columns, int32_t height) {
 // Products whose tiles of 16, 32 or 64 rows and columns all have a CU of their own go to the kernel whose
 // waves share out the reduction, in the smallest such tiles: what a CU reads is what takes its time.
 // Matrices from HBM, 7168 channels, us: 16 rows, 8192 columns in 16 x 32 12.6, 64 x 32 14.8, 64 x 64
-// 21.3; 32 rows in 32 x 32 14.3, 64 x 64 22.1; 100 rows, 4096 columns in 64 x 32 16.2, 64 x 64 22.5.
-// 64 x 128 tiles of the kernel above instead: 1 row, 4096 columns 20 (7.7 in 16 x 16), 256 rows 30 (25
+// 21.3; 32 rows in 32 x 32 14.3, 64 x 64 22.1; 100 rows, 4096 columns in 64 x 32 15.4, 64 x 64 22.5.
+// 64 x 128 tiles of the kernel above instead: 1 row, 4096 columns 20 (7.7 in 16 x 16), 256 rows 30 (23
 // in 64 x 64).  Experts of at most 32 rows are bound by reading their matrices, which those tiles do
 // faster where there are many (256 experts of 512 x 2048, 32 rows each: 49 us against 55).
 template <bool kGlu>

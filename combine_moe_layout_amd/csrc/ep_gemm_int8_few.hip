@@ -34,8 +34,10 @@ __global__ __launch_bounds__(waves_of(TM, TN) * 64, waves_of(TM, TN) / 4) void g
   constexpr int kSlotBytes = kLoads * 1024, kRingBytes = kSlots * kSlotBytes;
   __shared__ __align__(1024) char lds[kWaves * kRingBytes];
   static_assert(16 * TM * kPitch * 4 <= kRingBytes, "the sums take the ring's place");
+  // Up to four row tiles of a group at a column, so that an XCD reads that part of the matrix once: 256
+  // rows, 7168 x 4096, 22.6 us, row tile by row tile 24.7.
   Tile t;
-  if (!find_tile<1>(g.groups, 16 * TM, (g.out_cols + kOut - 1) / kOut, blockIdx.x, t)) return;
+  if (!find_tile<4, true>(g.groups, 16 * TM, (g.out_cols + kOut - 1) / kOut, blockIdx.x, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
   const int first = t.col * kOut;
