@@ -373,10 +373,9 @@ hipError_t launch_size(const GemmArgs& g, hipStream_t stream) {
   const int32_t low = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   for (int32_t width = 16; width <= 64; width *= 2)
     if (tiles(low, width) <= kChipCUs) return launch_gemm_int8_few(g, low, width, stream);
-  // Where 64 x 128 tiles would share CUs and 128 x 128 tiles do not, those: 7168 channels, 4096 columns,
-  // 640 rows 31 us (else 33), 1024 rows 34 (40); 4096 channels 20.5 (21.7), 22.5 (27.9); 2048 channels,
-  // 7168 columns, 300 rows 10.7 (12.2); 8 experts of 128 rows, 2048 x 4096, 21.6 (23.8).  Sharing CUs,
-  // they lose: 1280 rows of the first 46 (42).
+  // Where 64 x 128 tiles would share CUs and 128 x 128 tiles do not, those.  Matrices from HBM, 4096
+  // columns, us: 7168 channels, 640 rows 38 (else 44), 1024 rows 40 (55); 4096 channels 24 (27), 26 (35);
+  // 8 experts of 128 rows, 2048 x 4096, 21 (22).  Where neither share, 512 rows of the first 38 (31).
   if (rows > 32 && tiles(64, 128) > kChipCUs && tiles(128, 128) <= kChipCUs)
     return launch<kGlu, 4, 2, 2, 4>(g, 128, stream);
   int32_t height = 64;
