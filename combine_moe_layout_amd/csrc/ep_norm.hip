@@ -11,9 +11,11 @@
 // Two vectors to a lane (8192 x 7168: one vector 95 us, four 84; 2048 x 4096: 15.6, 13.1 with two, 12.1).
 //
 // Gradient, with D = sum(dx post y), everything recomputed from the forward's inputs:
-//   dx = d_out + r (pre dn) - x r^3 mean(pre dn x)        d_residual = alpha dx
-//   d_gate = s D       d_y = gate (s post dx - y s^3 D / hidden)
+//   dx = d_out + r (pre dn - x r (r mean(pre dn x)))      d_residual = alpha dx
+//   d_gate = s D       d_y = gate s (post dx - y s (s D / hidden))
 //   d_post = sum over rows of gate dx y s                 d_pre = sum over rows of dn x r
+// s and r are applied one at a time: their cubes leave fp32's range where rows' roots of mean squares
+// are past 1e12, and where they and eps are small.
 // A workgroup walks rows and keeps its sums of d_post and d_pre; they meet in a second kernel in a
 // fixed order, so the result does not depend on timing.  16,384 rows of 4096: 145 us (5.5 TB/s),
 // 344 us without the next row's loads in flight, 234 us with them but with the weights loaded for
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
       }
       row_sums(sums, lanes, part[turn][1]);
       const float r = inverse_rms(sums[0], a.hidden, a.eps);
-      const float back = r * r * r * (sums[1] * mean);
+      const float along = r * (sums[1] * mean);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float w[8], d[8];
@@ -300,8 +302,8 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
         unpack8<kF16>(nv[i], d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          dx[i][k] += fmaf(r, d[k] * w[k], -x[i][k] * back);
           x[i][k] *= r;
+          dx[i][k] = fmaf(r, fmaf(-x[i][k], along, d[k] * w[k]), dx[i][k]);
         }
         sum_pre.add(i, d, x[i]);
       }
@@ -338,14 +340,14 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
       if (a.d_gate != nullptr && lane == 0) a.d_gate[row] = s * dot[0];
     }
     if (has_y && a.d_y != nullptr) {
-      const float along = gate * s, back = has_post ? gate * (s * s * s) * (dot[0] * mean) : 0.0f;
+      const float along = has_post ? s * (dot[0] * mean) : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = lane + i * lanes;
         float f[8];
         unpack8<kF16>(yv[i], f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = fmaf(along, dx[i][k], -f[k] * back);
+        for (int k = 0; k < 8; ++k) f[k] = gate * s * fmaf(-f[k] * s, along, dx[i][k]);
         if (v < vecs) store_nt(static_cast<u32x4*>(a.d_y) + at + v, pack8<kF16>(f));
       }
     }
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
       unpack8<kF16>(p != nullptr ? static_cast<const u32x4*>(p)[at + v] : zero, f);
     };
     const float gate = a.gate != nullptr ? a.gate[row] : 1.0f;
-    float s = 1.0f, r = 0.0f, back = 0.0f;
+    float s = 1.0f, r = 0.0f, along = 0.0f;
     if (has_post) {
       float squares[1] = {0.0f};
 #pragma unroll 4
@@ -463,7 +465,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
       }
       row_sums(sums, lanes, part[turn][1]);
       r = inverse_rms(sums[0], a.hidden, a.eps);
-      back = r * r * r * (sums[1] * mean);
+      along = r * (sums[1] * mean);
     }
     const auto gradient = [&](int v, float (&x)[8], float (&dx)[8]) {
       vector(a.d_out, v, dx);
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
       float d[8];
       hidden(v, x, d);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dx[k] += fmaf(r, d[k], -x[k] * back);
+      for (int k = 0; k < 8; ++k) dx[k] = fmaf(r, fmaf(-x[k] * r, along, d[k]), dx[k]);
     };
     const auto add = [&](float* own, int v, const float (&p)[8], const float (&q)[8]) {
       f32x4* const to = reinterpret_cast<f32x4*>(own) + 2 * v;
@@ -514,7 +516,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
       if (a.d_gate != nullptr && threadIdx.x == 0) a.d_gate[row] = s * dot[0];
     }
     if (a.d_y == nullptr && a.d_residual == nullptr) continue;
-    const float along = gate * s, back_y = has_post ? gate * (s * s * s) * (dot[0] * mean) : 0.0f;
+    const float along_y = has_post ? s * (dot[0] * mean) : 0.0f;
 #pragma unroll 2
     for (int v = threadIdx.x; v < vecs; v += lanes) {
       float x[8], dx[8], f[8], w[8];
@@ -532,7 +534,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
         for (int k = 0; k < 8; ++k) dx[k] *= w[k];
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = fmaf(along, dx[k], -f[k] * back_y);
+      for (int k = 0; k < 8; ++k) f[k] = gate * s * fmaf(-f[k] * s, along_y, dx[k]);
       store_nt(static_cast<u32x4*>(a.d_y) + at + v, pack8<kF16>(f));
     }
   }

@@ -1,14 +1,16 @@
-"""The router at the ends of its range, against its definition in 64 bits."""
+"""The router and the block norms at the ends of their ranges, against the definitions in 64 bits."""
 import math
 
 import pytest
 import torch
 
 import block_ref as ref
+import test_gpu_block_norm as norms
 import test_gpu_route as routes
 from combine_moe_layout_amd import binding as B
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
 
 # groups of 2, 3 and 60 experts meet in LDS, groups of 8, 32 and 256 by lanes of 4, 8 and 16 experts
 GROUPS = [(4, 2, 1), (24, 8, 3), (64, 8, 3), (300, 5, 2), (512, 16, 4), (1024, 4, 2)]
@@ -32,3 +34,37 @@ def test_group_sums_past_fp32(E, groups, topk_groups, score):
             router = B.EpRouter(E, 2, routes.SCORES[score], groups, topk_groups, 2)
             idx, _ = routes.route(logits, "fp32", router, bias)
             assert torch.equal(idx, ref.choice(logits, bias, 2, score, groups, topk_groups, 2)), (sign, seed)
+
+
+@pytest.mark.parametrize("rows,H", [(5, 64), (9, 1032), (3, 8200), (3, 16392)])
+def test_norm_gradients_of_large_rows(rows, H):
+    """Rows whose root mean square is 1e12 to 1e16: sums of squares are in range, and the part of the
+    gradient along the row is as right as any other."""
+    print("[gpu-edges] large rows", rows, H, flush=True)
+    for kind, scale in ((k, s) for k in ("all", "post", "add", "first") for s in (1e12, 1e14, 1e15, 1e16)):
+        v = norms.inputs(rows, H, kind, BF)
+        for n in ("y", "residual"):
+            v[n] = None if v[n] is None else (v[n].float() * scale).to(BF)
+        if v["d_normed"] is not None:
+            v["d_out"] = None
+        want, size = norms.exact_gradients(v, 0.75), norms.sizes(v, 0.75)
+        got = norms.gradients(v, B.EP_BF16, BF, 0.75, B.EP_GRAD_F32)
+        for k in got:
+            norms.near(got[k], want[k], size[k], (kind, scale, k))
+
+
+@pytest.mark.parametrize("rows,H", [(5, 64), (9, 1032), (3, 8200), (3, 16392)])
+@pytest.mark.parametrize("eps", [1e-24, 1e-30, 1e-36])
+def test_norm_gradients_of_empty_rows_with_a_small_eps(rows, H, eps, monkeypatch):
+    """A row of zeros has an inverse root mean square of 1e12 to 1e18 and the gradients that go with it;
+    the weights' gradients do not see it."""
+    monkeypatch.setattr(norms, "EPS", eps)
+    for kind in ("all", "post", "add", "first"):
+        v = norms.inputs(rows, H, kind, BF)
+        for n in ("y", "residual"):
+            if v[n] is not None:
+                v[n][1] = 0
+        want, size = norms.exact_gradients(v, 0.75), norms.sizes(v, 0.75)
+        got = norms.gradients(v, B.EP_BF16, BF, 0.75, B.EP_GRAD_F32)
+        for k in got:
+            norms.near(got[k], want[k], size[k], (kind, k))
