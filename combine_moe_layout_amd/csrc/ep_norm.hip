@@ -340,14 +340,15 @@ __global__ __launch_bounds__(kPrefetch ? kMaxLanes / 2 : kMaxLanes) void block_n
       if (a.d_gate != nullptr && lane == 0) a.d_gate[row] = s * dot[0];
     }
     if (has_y && a.d_y != nullptr) {
-      const float along = has_post ? s * (dot[0] * mean) : 0.0f;
+      const float along = s * (dot[0] * mean);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = lane + i * lanes;
         float f[8];
         unpack8<kF16>(yv[i], f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = gate * s * fmaf(-f[k] * s, along, dx[i][k]);
+        for (int k = 0; k < 8; ++k)  // (without its norm y has no part in it: it may be infinite)
+          f[k] = gate * s * (has_post ? fmaf(-f[k] * s, along, dx[i][k]) : dx[i][k]);
         if (v < vecs) store_nt(static_cast<u32x4*>(a.d_y) + at + v, pack8<kF16>(f));
       }
     }
@@ -516,7 +517,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
       if (a.d_gate != nullptr && threadIdx.x == 0) a.d_gate[row] = s * dot[0];
     }
     if (a.d_y == nullptr && a.d_residual == nullptr) continue;
-    const float along_y = has_post ? s * (dot[0] * mean) : 0.0f;
+    const float along_y = s * (dot[0] * mean);
 #pragma unroll 2
     for (int v = threadIdx.x; v < vecs; v += lanes) {
       float x[8], dx[8], f[8], w[8];
@@ -534,7 +535,7 @@ __global__ __launch_bounds__(kMaxLanes) void block_norm_grad_wide_kernel(NormArg
         for (int k = 0; k < 8; ++k) dx[k] *= w[k];
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = gate * s * fmaf(-f[k] * s, along_y, dx[k]);
+      for (int k = 0; k < 8; ++k) f[k] = gate * s * (has_post ? fmaf(-f[k] * s, along_y, dx[k]) : dx[k]);
       store_nt(static_cast<u32x4*>(a.d_y) + at + v, pack8<kF16>(f));
     }
   }

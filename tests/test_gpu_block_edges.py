@@ -68,3 +68,14 @@ def test_norm_gradients_of_empty_rows_with_a_small_eps(rows, H, eps, monkeypatch
         got = norms.gradients(v, B.EP_BF16, BF, 0.75, B.EP_GRAD_F32)
         for k in got:
             norms.near(got[k], want[k], size[k], (kind, k))
+
+
+@pytest.mark.parametrize("H", [64, 1032, 8200, 16392])
+def test_gradient_by_an_infinite_y_without_its_norm(H):
+    """Without norms d_y = gate d_out and d_residual = alpha d_out, whatever y holds."""
+    v = norms.inputs(6, H, "gate", BF)
+    v["pre"] = v["d_normed"] = None
+    v["y"][1, 3], v["y"][2, H - 1], v["y"][4] = math.inf, math.nan, -math.inf
+    got = norms.gradients(v, B.EP_BF16, BF, 0.75, only=("y", "residual"))
+    assert torch.equal(got["y"], (v["d_out"].float() * v["gate"][:, None]).to(BF))
+    assert torch.equal(got["residual"], (v["d_out"].float() * 0.75).to(BF))
