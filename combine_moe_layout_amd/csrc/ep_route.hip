@@ -136,7 +136,7 @@ __device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(
 // 2^-24 of it, of its sum with the bias.  `unit` covers what two scores are off by: sigmoid scores
 // 2^-22 each; softmax scores 2^-18.8 of themselves (the terms and additions, 22 at most, of the sum over
 // all experts), two of which are at most 1 and at most twice the largest, 1 / sum.  Groups' scores of
-// two keys, n = 2: see sum_of_two.
+// two keys: see sum_of_two.
 __device__ __forceinline__ bool near(float unit, float larger, float smaller, float n) {
   return larger - smaller <= n * (unit + 0x1p-21f * fabsf(larger));
 }
@@ -146,10 +146,10 @@ __device__ __forceinline__ float near_unit(const RouteArgs& a, float sum) {
 
 // A group's score of its two largest keys: their sum, in float half of it, which stays in float's range.
 // The sum's roundings are 2^-24 (|one| + |two| + |sum|), at most 2^-23 (|two| + |sum|).  Where -two is at
-// most 2 |sum| + c, that is 2^-23 (3 |sum| + c) for each of two groups, and `near` of the halves with n = 2,
-// 4 units and 2 * 2^-21 |sum| between the sums, has room for it: 1.5 * 2^-21 |sum|, and of the units what
-// four scores leave (sigmoid 2^-20, so c = 1; softmax 2.8 units, so c = 2^22 units).  Otherwise float
-// cannot tell.
+// most 2 |sum| + c, that is 2^-23 (3 |sum| + c) for each of two groups, and `near` of the halves with 3/4
+// of a unit and n = 2, 3 units and 2 * 2^-21 |sum| between the sums, has room for it: 1.5 * 2^-21 |sum|, and
+// of the units what four scores leave (sigmoid 2^-21, so c = 1; softmax 1.8 units, so c = 2^22 units).
+// Otherwise float cannot tell.
 template <typename R>
 __device__ __forceinline__ R sum_of_two(R one, R two, bool softmax, float unit, bool& unsure) {
   constexpr R kPart = sizeof(R) == 4 ? 0.5 : 1.0;
@@ -267,7 +267,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         if (!better && o != g) behind = fmax(behind, other);
       }
       if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none)
-        unsure |= near(unit, (float)mine, (float)behind, a.group_top == 2 ? 2.0f : 1.0f);
+        unsure |= a.group_top == 2 ? near(0.75f * unit, (float)mine, (float)behind, 2.0f)
+                                   : near(unit, (float)mine, (float)behind, 1.0f);
       return ahead < a.topk_groups;
     };
     if (a.group_shift >= 0) {  // a group is 2^group_shift whole lanes
