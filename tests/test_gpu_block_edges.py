@@ -8,6 +8,7 @@ import block_ref as ref
 import test_gpu_block_norm as norms
 import test_gpu_route as routes
 from combine_moe_layout_amd import binding as B
+from products_ref import half_step
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -79,3 +80,50 @@ def test_gradient_by_an_infinite_y_without_its_norm(H):
     got = norms.gradients(v, B.EP_BF16, BF, 0.75, only=("y", "residual"))
     assert torch.equal(got["y"], (v["d_out"].float() * v["gate"][:, None]).to(BF))
     assert torch.equal(got["residual"], (v["d_out"].float() * 0.75).to(BF))
+
+
+@pytest.mark.parametrize("E,k", [(2, 1), (64, 1), (64, 2), (256, 8), (300, 3), (1000, 1)])
+@pytest.mark.parametrize("name", ["fp32", "bf16"])
+def test_gradient_of_confident_softmax(E, k, name):
+    """Shares of all experts where the chosen have nearly everything:
+       d_j = scale p_j (sum_i p_i (dw_j - dw_i) + q dw_j),  q = the share of those not chosen,
+    and no digits are lost on the way.  A share is a term over a sum, (R + 4) and (R + n + 4) steps of
+    2^-24 off, R the range of the logits (as for the weights in test_gpu_route); a term of the gradient
+    has two of them, and k + 6 sums and products."""
+    print("[gpu-edges] confident softmax", E, k, name, flush=True)
+    code, dt = routes.TYPES[name]
+    T, scale = 48, 2.5
+    g = routes.gen(E + k)
+    logits = torch.randn((T, E), device="cuda", generator=g)
+    first = torch.randint(0, E, (T,), device="cuda", generator=g)
+    gap = torch.linspace(8.0, 60.0, T, device="cuda")
+    for j in range(k):
+        logits[torch.arange(T, device="cuda"), (first + j * 7) % E] = gap + 0.5 * j
+    logits = logits.to(dt)
+    dw = torch.randn((T, k), device="cuda", generator=g)
+    if k > 1:
+        dw[::2, 1] = dw[::2, 0]                        # equal gradients: the difference is 0
+        dw[1::4, 1] = dw[1::4, 0] * (1 + 2.0 ** -20)   # and nearly equal ones
+    router = B.EpRouter(E, k, B.EP_SCORE_SOFTMAX, renormalize=False, scale=scale)
+    idx, _ = routes.route(logits, name, router)
+    given = [idx] if k < 3 else [idx, torch.cat([idx[:, :1], idx[:, :1], idx[:, 2:]], 1)]   # one of them twice
+    for at in given:
+        d = torch.full_like(logits, 7.0)
+        B.ep_route_grad(dw, logits, at, router, d, code)
+        p = ref.scores(logits, "softmax")
+        by = torch.zeros_like(p).scatter_add_(1, at, dw.double())
+        chosen = torch.zeros_like(p, dtype=torch.bool).scatter_(1, at, True)
+        q = torch.where(chosen, 0.0, p).sum(1, keepdim=True)
+        pc = torch.where(chosen, p, 0.0)
+        want, size = torch.empty_like(p), torch.empty_like(p)
+        for t in range(T):
+            c = chosen[t].nonzero()[:, 0]
+            diff = by[t, :, None] - by[t, None, c]
+            want[t] = scale * p[t] * ((pc[t, c] * diff).sum(1) + q[t] * by[t])
+            size[t] = scale * p[t] * ((pc[t, c] * diff.abs()).sum(1) + q[t] * by[t].abs())
+        size = torch.where(chosen, size, scale * p * (pc * by.abs()).sum(1, keepdim=True))
+        # (a sum of two dw is rounded: half a step of the largest, in both factors of a difference)
+        dup = 0.0 if at is idx else 2 * ref.STEP * scale * pc * by.abs().amax(1, keepdim=True)
+        tol = (2 * routes.steps(logits, E) + (k + 6) * ref.STEP) * size + dup + 2.0 ** -126
+        tol = tol + half_step(want.abs() + tol, dt)
+        assert ((d.double() - want).abs() <= tol).all(), ((d.double() - want).abs() / tol).max().item()
