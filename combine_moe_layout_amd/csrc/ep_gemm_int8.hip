@@ -293,8 +293,12 @@ struct Int8Gemm {
     const float* const col_scales = static_cast<const float*>(g.b_scales) + t.e * (g.b_stride / g.ldb);
     float scale[TM];
     f32x4 sums[TM][TN];
+    uint32_t large = 0;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) scale[i] = row_scales[min((i * WM + wm) * 16 + (lane & 15), t.rows - 1)];
+    for (int i = 0; i < TM; ++i) {
+      scale[i] = row_scales[min((i * WM + wm) * 16 + (lane & 15), t.rows - 1)];
+      large |= (uint32_t)split_scale(scale[i]) << i;
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -303,6 +307,12 @@ struct Int8Gemm {
 #pragma unroll
         for (int i = 0; i < TM; ++i) sums[i][j][c] = (float)acc[i][j][c] * scale[i] * col;
       }
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(large != 0) != 0, 0)) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sums[i][j] *= large >> i & 1 ? kLargePart : 1.0f;
+    }
     Store::store_tile(g, t, lds + wave * kWaveBytes, wm, wn, sums);
   }
 };

@@ -137,8 +137,10 @@ __global__ __launch_bounds__(waves_of(TM, TN) * 64, waves_of(TM, TN) / 4) void g
       sum += sums[c];
       if constexpr (kGlu) sum_up += sums[kOut + c];
     }
-    float z = (float)sum * row_scales[r] * col_scales[col], up = 0.0f;
-    if constexpr (kGlu) up = (float)sum_up * row_scales[r] * col_scales[n + col];
+    float row_scale = row_scales[r];
+    const float part = split_scale(row_scale) ? kLargePart : 1.0f;
+    float z = (float)sum * row_scale * col_scales[col] * part, up = 0.0f;
+    if constexpr (kGlu) up = (float)sum_up * row_scale * col_scales[n + col] * part;
     if (g.bias != nullptr) {
       z += elem_at<false>(g.bias, (int64_t)t.e * width + col);
       if constexpr (kGlu) up += elem_at<false>(g.bias, (int64_t)t.e * width + n + col);

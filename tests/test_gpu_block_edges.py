@@ -1,4 +1,5 @@
-"""The router and the block norms at the ends of their ranges, against the definitions in 64 bits."""
+"""The router, the block norms and the 8-bit products at the ends of their ranges, against the
+definitions in 64 bits."""
 import math
 
 import pytest
@@ -6,6 +7,7 @@ import torch
 
 import block_ref as ref
 import test_gpu_block_norm as norms
+import test_gpu_int8 as int8
 import test_gpu_route as routes
 from combine_moe_layout_amd import binding as B
 from products_ref import half_step
@@ -127,3 +129,28 @@ def test_gradient_of_confident_softmax(E, k, name):
         tol = (2 * routes.steps(logits, E) + (k + 6) * ref.STEP) * size + dup + 2.0 ** -126
         tol = tol + half_step(want.abs() + tol, dt)
         assert ((d.double() - want).abs() <= tol).all(), ((d.double() - want).abs() / tol).max().item()
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 208, 48), (16, 400, 4096), (200, 144, 4096), (700, 1040, 4096), (2300, 272, 4096)])
+@pytest.mark.parametrize("name", ["none", "swiglu"])
+def test_large_and_small_scales(T, K, N, name):
+    """Rows' scales of up to 2^117 with columns' as small, and the other way round: a sum times one scale
+    leaves fp32's range, the result does not.  (Below fp32's normal range a product is off by half of 2^-149.)"""
+    print("[gpu-edges] scales", T, K, N, name, flush=True)
+    N = N // 2 if name == "swiglu" else N
+    q, s, w, ws, bias = int8.operands(1, int8.width(N, name), K, T, T + N)
+    q[T // 2] = 0
+    out = torch.empty((T, N), dtype=BF, device="cuda")
+    pre = torch.empty((T, int8.width(N, name)), dtype=BF, device="cuda")
+    for half in (2.0 ** 64, 2.0 ** -52):
+        ws2 = ws[0] / half / half
+        for rows in (slice(None), slice(1, None, 2)):      # all of them, every other
+            s2 = s.clone()
+            s2[rows] = s2[rows] * half * half
+            z, off = int8.exact_product(q, s2, w[0], ws2, bias[0])
+            off = off + 2.0 ** -149
+            B.ep_linear_int8(q, s2, w[0], ws2, out, act=int8.ACTS[name], bias=bias[0], preact=pre)
+            # (the rows left as they were times 2^104: what they give is not of interest)
+            at = slice(None) if half > 1 else rows
+            int8.check(pre[at], z[at], off[at], "preact")
+            int8.check(out[at], int8.act(z, name)[at], int8.act_error(z, off, name)[at], "out")
