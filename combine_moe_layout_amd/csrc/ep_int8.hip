@@ -152,12 +152,14 @@ template <bool kF16>
 hipError_t launch(const void* x, int64_t rows, int32_t hidden, int32_t k, const int32_t* slots,
                   const RowGroups& groups, void* codes, float* scales, hipStream_t stream) {
   const int vecs = hidden / 16;
-  // Rows where they stand: two vectors to a lane beyond one wave's 64 (8192 x 7168: 31.4 us, 37.6
-  // with one; four up to one wave's 256: 65536 x 2048 in 71.4, 74.0).  Dispatch: one as long as a
-  // workgroup holds the row, for its k stores to be spread wide (8192 tokens of 4096 to 6 experts:
-  // 41 us, 64 with four).
+  // Rows where they stand: two vectors to a lane beyond one wave's 64 (8192 x 7168: 30.5 us, 35.1 with one
+  // and 34 with four; 65,536 x 2048: 71.5, 77.5 and 77).  Four, so that a row is one wave's and needs no
+  // barrier, where that saves a second wave with half its lanes idle and there are rows enough: 65,536 x
+  // 2064 and 2560 80 and 91.5 us (87 and 99 with two), 16,384 x 2560 26.4 (26.4); but 8192 x 2560 17.6
+  // (16.6), 16 x 4096 7.2 (4.9), 65,536 x 3584 131 (122).  Dispatch: one as long as a workgroup holds the
+  // row, for its k stores to be spread wide (8192 tokens of 4096 to 6 experts: 41 us, 64 with four).
   int vectors = 1;
-  if (slots == nullptr && vecs > 64) vectors = vecs > 128 && vecs <= 256 ? 4 : 2;
+  if (slots == nullptr && vecs > 64) vectors = vecs > 128 && vecs < 192 && rows >= 16384 ? 4 : 2;
   while ((vecs + vectors - 1) / vectors > kMaxLanes) vectors *= 2;
   const int lanes = ((vecs + vectors - 1) / vectors + 63) / 64 * 64;
   const int here = lanes == 64 ? 4 : 1;
