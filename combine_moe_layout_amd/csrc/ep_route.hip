@@ -13,10 +13,10 @@
 // the token's lanes by DPP moves on order-preserving integers, and the lowest lane that has it
 // (lanes are in the experts' order) owns it: the tie goes to the lower index by itself.
 //
-// The order is that of the keys as real numbers.  Logits are compared as they are.  Keys with
-// scores in them are made in fp32 first; choices go on past the k-th while the next might belong
-// before it, and where two candidates are closer than fp32 can tell (for random logits and biases
-// at 256 experts one token in 1000), the candidates' keys alone are made again in fp64.  Where that is
+// The order is that of the keys in fp64.  Logits are compared as they are.  Keys with scores in
+// them are made in fp32 first; choices go on past the k-th while the next might belong before it,
+// and where two candidates are closer than fp32 can tell (for random logits and biases at 256
+// experts one token in 1000), the candidates' keys alone are made again in fp64.  Where that is
 // not enough -- groups too close to tell, more candidates than lanes -- the wave does all of
 // it in fp64.
 //
@@ -132,7 +132,7 @@ __device__ __forceinline__ float score_sigmoid(float l) {
 }
 __device__ __forceinline__ double score_sigmoid(double l) { return 1 / (1 + exp(-l)); }
 
-// Whether two float keys may be in the other order as real numbers.  A key is a score and half a step,
+// Whether two float keys may be in the other order in fp64.  A key is a score and half a step,
 // 2^-24 of it, of its sum with the bias.  `unit` covers what two scores are off by: sigmoid scores
 // 2^-22 each; softmax scores 2^-18.8 of themselves (the terms and additions, 22 at most, of the sum over
 // all experts), two of which are at most 1 and at most twice the largest, 1 / sum.  Groups' scores of
@@ -338,7 +338,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
     }
     return unsure;
   }
-  // The k largest, and those after them that may belong before the k-th as real numbers.
+  // The k largest, and those after them that may belong before the k-th in fp64.
   K kept = none_key, last = none_key;  // of choice `lane`, of choice k - 1
   int count = a.k;
   for (int j = 0;; ++j) {

@@ -571,8 +571,11 @@ typedef struct ep_router {
  *      num_groups); with group_top 2 and no bias a group's score is of s, not of logits;
  *   2. topk_idx[t] = the experts of the k largest keys among those groups, descending;
  *   3. topk_weights[t, j] = scale * s[topk_idx[t, j]], renormalised if asked for.
- * The bias (for balance) takes part in the choice alone.  Keys are compared as real numbers,
- * not as rounded to fp32; equal ones go to the lower index (of experts, of groups).
+ * The bias (for balance) takes part in the choice alone.  Logits are compared as they are; keys
+ * with scores in them, and groups' sums of two, as fp64 has them (a score rounded to fp64, then
+ * its sums), not as rounded to fp32.  Equal ones go to the lower index (of experts, of groups):
+ * with a bias those are also scores that differ by less than fp64 shows beside it (2^-53 of it),
+ * and the sigmoids of logits past 37, which are 1.
  * An expert with a logit of -inf or NaN, or a key of -inf or NaN, is never chosen and has a
  * score of 0; a logit of +inf counts as the largest fp32 value.  Where a token has fewer
  * than k experts to choose from, the last entries are -1 (unrouted) with a weight of 0.

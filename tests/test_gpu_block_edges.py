@@ -39,6 +39,23 @@ def test_group_sums_past_fp32(E, groups, topk_groups, score):
             assert torch.equal(idx, ref.choice(logits, bias, 2, score, groups, topk_groups, 2)), (sign, seed)
 
 
+@pytest.mark.parametrize("E,k,groups,topk_groups,group_top", [(64, 6, 1, 1, 1), (256, 8, 8, 3, 2), (250, 5, 5, 2, 1)])
+def test_keys_that_fp64_cannot_tell(E, k, groups, topk_groups, group_top):
+    """Sigmoids of logits past 37 are 1 in fp64, and scores beside a bias of 1e17 add nothing: with a bias
+    those are ties and go to the lower index, without one the logits decide."""
+    logits = 38 + 22 * torch.rand((30, E), device="cuda", generator=routes.gen(E))
+    router = B.EpRouter(E, k, B.EP_SCORE_SIGMOID, groups, topk_groups, group_top)
+    first = torch.arange(k, device="cuda").expand(30, k)
+    for l, b in ((logits, 0.0), (logits, 0.5), (logits - 49, 1e17)):
+        idx, _ = routes.route(l, "fp32", router, torch.full((E,), b, device="cuda"))
+        assert torch.equal(idx, first), b
+    if group_top == 1:
+        idx, _ = routes.route(logits, "fp32", router)
+        assert torch.equal(idx, ref.choice(logits, None, k, "sigmoid", groups, topk_groups, group_top))
+        if groups == 1:
+            assert torch.equal(idx, torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k])
+
+
 @pytest.mark.parametrize("rows,H", [(5, 64), (9, 1032), (3, 8200), (3, 16392)])
 def test_norm_gradients_of_large_rows(rows, H):
     """Rows whose root mean square is 1e12 to 1e16: sums of squares are in range, and the part of the
