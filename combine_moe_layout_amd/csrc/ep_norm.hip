@@ -20,7 +20,7 @@
 // fixed order, so the result does not depend on timing.  16,384 rows of 4096: 145 us (5.5 TB/s),
 // 344 us without the next row's loads in flight, 234 us with them but with the weights loaded for
 // each row, behind them.  More than 8192 channels leave no registers for that, and up to 16,384 the
-// sums are in LDS (2048 x 16,384: 126 us; 176 in registers, which spilled; 300 by the wide rows'
+// sums are in LDS (2048 x 16,384: 121 us; 176 in registers, which spilled; 300 by the wide rows'
 // kernel, which more channels go to).
 #include "ep_norm.h"
 

@@ -24,9 +24,10 @@
 // where every chosen score underflows.
 //
 // Bound by the rounds of choosing: a dozen vector instructions of maximum, ballot and removal each,
-// with lanes' keys sorted by fours beforehand.  8192 tokens, 256 experts, top-8, fp32: 6.9 us by
-// logits, 10.1 with a bias (14.1 with every near pair redone in fp64 as a whole token), 12.2 with
-// groups too; the reading takes 1.8.  65,536 tokens, 64 experts, top-6: 9.0 us, gradient 8.3.
+// with lanes' keys sorted by fours beforehand.  8192 tokens, 256 experts, top-8, fp32: 6.8 us by
+// logits, 10.5 with a bias, 12.3 with groups too (11.5 to 13.9 for other logits: a wave that goes to
+// fp64 takes 2 us); the reading takes 1.8.  With every near pair redone in fp64 as a whole token, a
+// bias took 14.1, where it now took 10.1.  65,536 tokens, 64 experts, top-6: 9.1 us, gradient 8.1.
 #include "ep_route.h"
 
 namespace ep {
@@ -255,6 +256,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
   }
   if (grouped) {
     R* const score = shared;  // [groups]: the largest key, or the sum of the two largest
+    const float group_unit = a.group_top == 2 ? 0.75f * unit : unit, group_n = a.group_top == 2 ? 2.0f : 1.0f;
     // Whether group g stays: fewer than topk_groups are ahead of it.  The last that stays looks
     // how far the best of those that do not is behind it.
     const auto stays = [&](int g, R mine) {
@@ -267,8 +269,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[V], 
         if (!better && o != g) behind = fmax(behind, other);
       }
       if (kFloat && scored && ahead == a.topk_groups - 1 && behind > none)
-        unsure |= a.group_top == 2 ? near(0.75f * unit, (float)mine, (float)behind, 2.0f)
-                                   : near(unit, (float)mine, (float)behind, 1.0f);
+        unsure |= near(group_unit, (float)mine, (float)behind, group_n);
       return ahead < a.topk_groups;
     };
     if (a.group_shift >= 0) {  // a group is 2^group_shift whole lanes
@@ -471,13 +472,17 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(const float* __res
   const int64_t t = (int64_t)blockIdx.x * kTokens + local;
   const int64_t from = t < tokens ? t : tokens - 1;
   float2* const mine = pairs + local * L;
-  // (Loads without branches: behind them the kernel's arguments came one by one, 0.3 us.)
-  const int64_t pair = from * a.k + min(lane, a.k - 1), e = idx[pair];
-  const float given = dweights[pair];
-  const bool real = lane < a.k && e >= 0 && e < a.E;
-  const float logit = usable(logit_at<kType>(logits, from * a.E + (real ? e : 0)));
-  const Choice c = real ? Choice{(int32_t)e, logit} : Choice{-1, -INFINITY};
-  const float dw = c.logit > -INFINITY ? given : 0.0f;
+  // (One branch: behind one for each load the kernel's arguments came one by one too, 0.4 us.)
+  Choice c = {-1, -INFINITY};
+  float dw = 0.0f;
+  if (lane < a.k) {
+    const int64_t pair = from * a.k + lane, e = idx[pair];
+    const float given = dweights[pair];
+    const bool known = e >= 0 && e < a.E;
+    const float logit = usable(logit_at<kType>(logits, from * a.E + (known ? e : 0)));
+    if (known) c = Choice{(int32_t)e, logit};
+    if (c.logit > -INFINITY) dw = given;
+  }
   // The sum of `v` over an expert's entries, and whether this is the first of them.
   const auto by_expert = [&](float v, bool& first_entry) {
     mine[lane] = float2{__int_as_float(c.expert), v};
